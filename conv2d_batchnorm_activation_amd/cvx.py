@@ -29,7 +29,7 @@ CVX_RES_NONE, CVX_RES_BEFORE_ACT, CVX_RES_AFTER_ACT = 0, 1, 2
 CVX_L_CONV, CVX_L_GAP, CVX_L_FC, CVX_L_PREPROC = 0, 1, 2, 3
 CVX_INPUT, CVX_NO_RES = -1, -2
 CVX_W_OIHW, CVX_W_PACKED = 0, 1
-CVX_DT_F32, CVX_DT_F16, CVX_DT_BF16 = 0, 1, 2
+CVX_DT_F32, CVX_DT_F16, CVX_DT_BF16, CVX_DT_E4M3 = 0, 1, 2, 3
 STATUS_NAMES = {0: "CVX_OK", -1: "CVX_ERR_NULL", -2: "CVX_ERR_SHAPE", -3: "CVX_ERR_UNSUPPORTED",
                 -4: "CVX_ERR_ALIGN", -5: "CVX_ERR_ALIAS", -6: "CVX_ERR_WORKSPACE",
                 -7: "CVX_ERR_HIP", -8: "CVX_ERR_ARG", -9: "CVX_ERR_SCRATCH"}
@@ -49,11 +49,25 @@ class cvx_layer(ctypes.Structure):
                 ("mean", ctypes.c_float * 3), ("std", ctypes.c_float * 3)]
 
 
+class cvx_rmsnorm_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("rows", "c", "dtype", "out_dtype")] + \
+        [("eps", ctypes.c_float)] + \
+        [(f, ctypes.c_long) for f in ("x_stride", "res_stride", "sum_stride", "y_stride")]
+
+
+class cvx_linear_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in
+                ("tokens", "c_in", "c_out", "dtype", "x_dtype", "act", "res_mode", "rank", "n_adapters")] + \
+        [(f, ctypes.c_long) for f in ("x_stride", "res_stride", "y_stride")]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
 _DP = ctypes.POINTER(cvx_conv_desc)
 _LP = ctypes.POINTER(cvx_layer)
+_RP = ctypes.POINTER(cvx_rmsnorm_desc)
+_NP = ctypes.POINTER(cvx_linear_desc)
 
 lib.cvx_status_str.argtypes = [_I]
 lib.cvx_status_str.restype = ctypes.c_char_p
@@ -94,6 +108,14 @@ lib.cvx_nhwc_pack_weights.argtypes = [_DP, _I, _P, _P, _P]
 lib.cvx_nhwc_pack_weights.restype = _I
 lib.cvx_conv_bn_act_nhwc.argtypes = [_DP, _I, _P, _P, _P, _P, _P, _P, _P]
 lib.cvx_conv_bn_act_nhwc.restype = _I
+lib.cvx_rmsnorm.argtypes = [_RP, _P, _P, _P, _P, _P, _P, _P]
+lib.cvx_rmsnorm.restype = _I
+lib.cvx_linear_workspace_bytes.argtypes = [_NP]
+lib.cvx_linear_workspace_bytes.restype = _Z
+lib.cvx_linear_plan.argtypes = [_NP, ctypes.c_char_p, _I]
+lib.cvx_linear_plan.restype = _I
+lib.cvx_linear.argtypes = [_NP] + [_P] * 12 + [_Z, _P]
+lib.cvx_linear.restype = _I
 lib.cvx_static_scratch_bytes.argtypes = []
 lib.cvx_static_scratch_bytes.restype = _Z
 lib.cvx_forward_noalloc.argtypes = [_LP, _I, _P, _P, _P]
@@ -106,7 +128,8 @@ EXPORTS = ("cvx_status_str", "cvx_version", "cvx_conv_out_shape", "cvx_conv_plan
            "cvx_conv_workspace_bytes", "cvx_packed_weights_bytes", "cvx_pack_weights", "cvx_fold_bn", "cvx_conv_bn_act", "cvx_preprocess_u8",
            "cvx_gap_fc", "cvx_forward_out_shape", "cvx_forward_workspace_bytes", "cvx_forward_plan",
            "cvx_forward", "cvx_nhwc_packed_weights_bytes", "cvx_nhwc_plan", "cvx_nhwc_pack_weights",
-           "cvx_conv_bn_act_nhwc", "cvx_static_scratch_bytes", "cvx_forward_noalloc",
+           "cvx_conv_bn_act_nhwc", "cvx_rmsnorm", "cvx_linear_workspace_bytes", "cvx_linear_plan", "cvx_linear",
+           "cvx_static_scratch_bytes", "cvx_forward_noalloc",
            "cvx_workgroup_xcds")
 
 
@@ -285,3 +308,41 @@ def cvx_conv_bn_act_nhwc(desc: cvx_conv_desc, dtype: int, x, w_packed, scale, bi
     _check(lib.cvx_conv_bn_act_nhwc(ctypes.byref(desc), dtype, _ptr(x), _ptr(w_packed), _ptr(scale),
                                     _ptr(bias), _ptr(residual), _ptr(y), _stream(stream)),
            "cvx_conv_bn_act_nhwc")
+
+
+def make_rmsnorm_desc(rows, c, dtype, out_dtype=None, eps=1e-6, x_stride=0, res_stride=0, sum_stride=0,
+                      y_stride=0) -> cvx_rmsnorm_desc:
+    return cvx_rmsnorm_desc(rows, c, dtype, dtype if out_dtype is None else out_dtype, eps, x_stride, res_stride,
+                            sum_stride, y_stride)
+
+
+def cvx_rmsnorm(desc: cvx_rmsnorm_desc, x, residual, gamma, sum_out, y, y_scale=None, stream=None) -> None:
+    _check(lib.cvx_rmsnorm(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum_out), _ptr(y),
+                           _ptr(y_scale), _stream(stream)), "cvx_rmsnorm")
+
+
+def make_linear_desc(tokens, c_in, c_out, dtype, x_dtype=None, act=CVX_ACT_NONE, res_mode=CVX_RES_NONE, rank=0,
+                     n_adapters=0, x_stride=0, res_stride=0, y_stride=0) -> cvx_linear_desc:
+    return cvx_linear_desc(tokens, c_in, c_out, dtype, dtype if x_dtype is None else x_dtype, act, res_mode, rank,
+                           n_adapters, x_stride, res_stride, y_stride)
+
+
+def cvx_linear_workspace_bytes(desc: cvx_linear_desc) -> int:
+    return lib.cvx_linear_workspace_bytes(ctypes.byref(desc))
+
+
+def cvx_linear_plan(desc: cvx_linear_desc) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.cvx_linear_plan(ctypes.byref(desc), buf, 256), "cvx_linear_plan")
+    return buf.value.decode()
+
+
+def cvx_linear(desc: cvx_linear_desc, x, w, y, x_scale=None, scale=None, bias=None, residual=None, lora_a=None,
+               lora_b=None, lora_alpha=None, lora_id=None, workspace=None, ws_bytes: Optional[int] = None,
+               stream=None) -> None:
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None or isinstance(workspace, int) else \
+            workspace.numel() * workspace.element_size()
+    _check(lib.cvx_linear(ctypes.byref(desc), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(scale), _ptr(bias),
+                          _ptr(residual), _ptr(lora_a), _ptr(lora_b), _ptr(lora_alpha), _ptr(lora_id), _ptr(y),
+                          _ptr(workspace), ws_bytes, _stream(stream)), "cvx_linear")

@@ -335,6 +335,120 @@ CVX_API cvx_status cvx_conv_bn_act_nhwc(const cvx_conv_desc *d, int dtype, const
                                         const void *w_packed, const float *scale, const float *bias,
                                         const void *residual, void *y, void *stream);
 
+/* ------------------------------------------------ operators on tokens
+ * A channels-last tensor with its pixels as rows, [rows][channels]: a 1x1 layer
+ * is then a projection of every row, and the rows may as well be the tokens of
+ * a sequence model.  The two operators here are such a projection in 16 or 8
+ * bits, with low-rank adapters for many requests at once, and the norm between
+ * projections, whose 8-bit output with a scale per row the projection reads.
+ * Rows may lie further apart than they are wide (a `*_stride` of the
+ * descriptor, in elements; 0 = dense), so a slice of a wider tensor's channels
+ * is an operand as it is.  Where two operands must not overlap, what counts is
+ * the range from an operand's first byte to its last. */
+
+/* Element type of 8-bit values: e4m3 (4 exponent bits, 3 fraction bits, largest
+ * value 448, no infinities).  Only the operators of this section take it. */
+enum { CVX_DT_E4M3 = 3 };
+
+typedef struct cvx_rmsnorm_desc {
+    int rows, c;        /* x [rows][c]; both at least 1                          */
+    int dtype;          /* CVX_DT_F32, _F16 or _BF16: x, residual, sum           */
+    int out_dtype;      /* type of y: dtype, or CVX_DT_E4M3                      */
+    float eps;          /* > 0                                                   */
+    long x_stride, res_stride, sum_stride, y_stride; /* row strides, 0 or >= c  */
+} cvx_rmsnorm_desc;
+
+/*
+ * cvx_rmsnorm -- residual addition and root-mean-square norm of every row, in
+ * one pass over the data and one launch:
+ *     h = x + residual                     (h = x without a residual)
+ *     q = 1 / sqrt(mean_i(h_i^2) + eps)
+ *     sum = h,  y_i = h_i * gamma_i * q    each rounded once to its type
+ * h is not rounded before the norm; sums and products are taken in 64 bits, so
+ * no finite row overflows them.  With out_dtype = CVX_DT_E4M3,
+ * u_i = h_i*gamma_i and t = max_i |u_i|,
+ *     y_i = e4m3(u_i * (448/t)),  y_scale = t*q/448     (t = 0: zeros)
+ * so that y_i * y_scale is the norm's output; q, which depends on the whole
+ * row's sum, cancels in the codes.
+ * A row that holds a NaN gives NaN throughout (8 bits: a NaN scale); one that
+ * holds an infinity gives NaN in its place and zeros elsewhere (8 bits: a NaN
+ * scale); other rows are not touched by it.
+ *   x, residual : device [rows][c] of dtype, aligned to an element; residual may be NULL.
+ *   gamma       : device fp32 [c].
+ *   sum         : device [rows][c] of dtype, or NULL when h is not wanted.  May be the
+ *                 same tensor as x or as residual (same address and stride).
+ *   y           : device [rows][c] of out_dtype, aligned to an element.
+ *   y_scale     : device fp32 [rows]; required iff out_dtype is CVX_DT_E4M3.
+ * y, y_scale and sum must not overlap one another or, but for sum as said, an input.
+ * Rows aligned to 16 bytes are fastest; others give the same results.
+ * Errors: CVX_ERR_NULL, CVX_ERR_SHAPE (rows or c < 1, a stride between 0 and c,
+ * more than 2^40 elements from first to last), CVX_ERR_ARG (types, eps),
+ * CVX_ERR_ALIGN, CVX_ERR_ALIAS, CVX_ERR_HIP.
+ */
+CVX_API cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc *d, const void *x, const void *residual,
+                               const float *gamma, void *sum, void *y, float *y_scale, void *stream);
+
+typedef struct cvx_linear_desc {
+    int tokens;         /* rows of x and y, 1 to 2^24                             */
+    int c_in, c_out;    /* channels, at most 2^20 each                            */
+    int dtype;          /* CVX_DT_F16 or _BF16: y, residual, adapters             */
+    int x_dtype;        /* type of x and w: dtype, or CVX_DT_E4M3                 */
+    int act;            /* CVX_ACT_*                                              */
+    int res_mode;       /* CVX_RES_*                                              */
+    int rank;           /* rank of the adapters, 0 = no adapters                  */
+    int n_adapters;     /* adapters held in lora_a and lora_b (0 when rank is 0)  */
+    long x_stride, res_stride, y_stride; /* row strides, 0 or >= the channels, at most 2^21 */
+} cvx_linear_desc;
+
+/* Workspace bytes cvx_linear needs for `d` (0 when it needs none, or on an
+ * invalid descriptor).  Host only. */
+CVX_API size_t cvx_linear_workspace_bytes(const cvx_linear_desc *d);
+
+/* Host-only query: the kernels and tiles chosen for `d`, like cvx_conv_plan. */
+CVX_API cvx_status cvx_linear_plan(const cvx_linear_desc *d, char *buf, int buf_len);
+
+/*
+ * cvx_linear -- projection of tokens with the layer epilogue, and low-rank
+ * adapters of many requests beside it:
+ *     v_t[r]   = x_scale[t] * sum_i lora_a[d][r][i] * x[t][i]          d = lora_id[t]
+ *     z_t[o]   = scale[o] * x_scale[t] * sum_i w[o][i]*x[t][i] + bias[o]
+ *                + lora_alpha[d] * sum_r lora_b[d][o][r] * v_t[r]
+ *     y        = act(z [+ residual]) [+ residual]                      by d->res_mode
+ * Products are accumulated in fp32 (with 8-bit operands and more than 64 tokens,
+ * the matrix cores align the products of eight consecutive channels to the
+ * largest of them and drop what lies 2^-13 below it), v is kept in fp32 between its two products
+ * (as two 16-bit values whose sum it is, where the matrix cores take it), and y
+ * is rounded once.  A token without an adapter is one whose id is negative or
+ * not below n_adapters.  An adapter's values, infinities and NaN included, reach
+ * the tokens that name it and no others.  Results do not depend on timing.
+ *   x          : device [tokens][c_in] of x_dtype, 16-byte aligned rows.
+ *   x_scale    : device fp32 [tokens]; required iff x_dtype is CVX_DT_E4M3
+ *                (cvx_rmsnorm's y and y_scale are such operands).
+ *   w          : device [c_out][c_in] of x_dtype, dense, 16-byte aligned.
+ *   scale, bias: device fp32 [c_out], 16-byte aligned; NULL means 1 and 0.  8-bit
+ *                weights have their per-channel scales in `scale`.
+ *   residual   : device [tokens][c_out] of dtype; required iff res_mode != CVX_RES_NONE.
+ *   lora_a     : device [n_adapters][rank][c_in] of dtype, dense, 16-byte aligned.
+ *   lora_b     : device [n_adapters][c_out][rank] of dtype, dense, 16-byte aligned.
+ *   lora_alpha : device fp32 [n_adapters], or NULL for 1.
+ *   lora_id    : device int32 [tokens].  lora_a, lora_b and lora_id are required iff rank > 0.
+ *   y          : device [tokens][c_out] of dtype, 8-byte aligned rows; must not overlap anything read.
+ *   workspace  : device scratch of cvx_linear_workspace_bytes(d) bytes, 16-byte
+ *                aligned (may be NULL when that is 0); contents on entry are
+ *                ignored.  Two calls in flight at once must not share one.
+ * Supported: c_in a multiple of 8 (16 in 8 bits), c_out a multiple of 4, rank a
+ * multiple of 8 up to 128 (adapters of lower rank are padded with zero rows and
+ * columns), x_stride a multiple of 8 (16 in 8 bits), y_stride and res_stride
+ * multiples of 4; else CVX_ERR_UNSUPPORTED.
+ * Errors otherwise: CVX_ERR_NULL, CVX_ERR_SHAPE, CVX_ERR_ARG (types, act,
+ * res_mode, a rank without adapters or adapters without a rank), CVX_ERR_ALIGN,
+ * CVX_ERR_ALIAS, CVX_ERR_WORKSPACE, CVX_ERR_HIP.
+ */
+CVX_API cvx_status cvx_linear(const cvx_linear_desc *d, const void *x, const float *x_scale, const void *w,
+                              const float *scale, const float *bias, const void *residual,
+                              const void *lora_a, const void *lora_b, const float *lora_alpha,
+                              const int *lora_id, void *y, void *workspace, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------ placement report */
 /*
  * cvx_workgroup_xcds -- where a launch's workgroups run.  Launches n_workgroups
