@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
     constexpr int STEPS = X8 ? 2 : 4;
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[(BM + BN) * 128];
     __shared__ __attribute__((aligned(1024))) unsigned char buf1[(BM + BN) * 128];
+    __shared__ float down_lds[V16<T>::BF ? 1 : BN];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;
@@ -76,25 +77,34 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
     const unsigned cb = (unsigned)a.cin * XB, pitch = (unsigned)a.xs * XB;
     const int mrows = a.cout - m0 < BM ? a.cout - m0 : BM;
     const int nrows = a.tokens - n0 < BN ? a.tokens - n0 : BN;
-    const rsrc_t rw = make_rsrc(static_cast<const char*>(a.w) + (long)m0 * cb, (unsigned)mrows * cb);
-    const rsrc_t rx = make_rsrc(static_cast<const char*>(a.x) + (long)n0 * pitch, (unsigned)(nrows - 1) * pitch + cb);
+    const char* wt = static_cast<const char*>(a.w) + (long)(m0 + 8 * wave) * cb;
+    const char* xt = static_cast<const char*>(a.x) + (long)(n0 + 8 * wave) * pitch;
     const unsigned piece = (unsigned)((lane & 7) ^ (lane >> 3)) * 16;
-    const unsigned wo = (unsigned)(8 * wave + (lane >> 3)) * cb + piece;
-    const unsigned xo = (unsigned)(8 * wave + (lane >> 3)) * pitch + piece;
+    const unsigned wo = (unsigned)(lane >> 3) * cb + piece;
+    const unsigned xo = (unsigned)(lane >> 3) * pitch + piece;
     const int nst = (int)((cb + 127) / 128);
 
-    // rows past the operand are past its descriptor's range, pieces past the row are sent there
+    // Eight rows a fetch.  Each has a descriptor of its own, which ends with the
+    // operand's rows, so what a lane holds is one offset an operand; pieces past
+    // the end of a row are sent out of range.
     auto issue = [&](int st, unsigned char* buf) {
-        const unsigned kb = (unsigned)st * 128;
-        const bool live = kb + piece < cb;
+        const unsigned kb = (unsigned)st * 128 < cb ? (unsigned)st * 128 : 0u;  // past the end: nothing is live
+        const bool live = (unsigned)st * 128 + piece < cb;
+        const unsigned wl = live ? wo : kOOB, xl = live ? xo : kOOB;
 #pragma unroll
-        for (int i = 0; i < 2 * MB; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(buf + 1024 * (wave + 4 * i)), 16,
-                                                     live ? wo + 32 * i * cb + kb : kOOB, 0, 0, 0);
+        for (int i = 0; i < 2 * MB; ++i) {
+            const int left = mrows - 8 * wave - 32 * i;
+            const unsigned n = left <= 0 ? 0u : (unsigned)(left < 8 ? left : 8) * cb - kb;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wt + (long)(32 * i) * cb + kb, n),
+                                                     (lds_void*)(buf + 1024 * (wave + 4 * i)), 16, wl, 0, 0, 0);
+        }
 #pragma unroll
-        for (int i = 0; i < 2 * NB; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(buf + BM * 128 + 1024 * (wave + 4 * i)), 16,
-                                                     live ? xo + 32 * i * pitch + kb : kOOB, 0, 0, 0);
+        for (int i = 0; i < 2 * NB; ++i) {
+            const int left = nrows - 8 * wave - 32 * i;
+            const unsigned n = left <= 0 ? 0u : (unsigned)((left < 8 ? left : 8) - 1) * pitch + cb - kb;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xt + (long)(32 * i) * pitch + kb, n),
+                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + 4 * i)), 16, xl, 0, 0, 0);
+        }
     };
     unsigned slot[4];
 #pragma unroll
@@ -143,6 +153,25 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
                     acc[m][n] = mma32<T>(A[m], B[n], acc[m][n]);
             }
     };
+    // Orders a step's instructions: the reads of the next operands and the fetches
+    // of a later stage between the matrix instructions.
+    auto mix = [&](auto fetches) {
+        constexpr int READS = (X8 ? 2 : 1) * (MB + NB), MUL = MB * NB, F = decltype(fetches)::value;
+        constexpr int OTHER = READS + F;
+#pragma unroll
+        for (int i = 0; i < MUL; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+#pragma unroll
+            for (int o = i * OTHER / MUL; o < (i + 1) * OTHER / MUL; ++o) {
+                if (o < READS)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                else
+                    __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+            }
+        }
+    };
+    typedef std::integral_constant<int, 0> no_fetch;
+    typedef std::integral_constant<int, 2 * (MB + NB)> fetch;
     auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
 #pragma unroll
         for (int s = 0; s + 1 < STEPS; ++s) {
@@ -153,66 +182,52 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
                 read(cur, s + 1, A1, B1);
                 mul(A0, B0);
             }
+            mix(no_fetch());
         }
         __builtin_amdgcn_s_waitcnt(0);  // the next stage has arrived, this wave has read the current one
         lds_barrier();
-        if (st + 2 < nst) issue(st + 2, cur);
-        if (st + 1 < nst) read(nxt, 0, A0, B0);
+        issue(st + 2, cur);
+        read(nxt, 0, A0, B0);
         mul(A1, B1);
+        mix(fetch());
     };
+    // An odd number of stages ends with one of zeros; so do the fetches past the last.
     issue(0, buf0);
     __builtin_amdgcn_s_waitcnt(0);
     lds_barrier();
-    if (nst > 1) issue(1, buf1);
+    issue(1, buf1);
     read(buf0, 0, A0, B0);
     for (int st = 0; st < nst; st += 2) {
         stage(st, buf0, buf1);
-        if (st + 1 < nst) stage(st + 1, buf1, buf0);
+        stage(st + 1, buf1, buf0);
     }
+    __builtin_amdgcn_s_waitcnt(0);  // no fetch is under way when LDS is used again
+    lds_barrier();
 
-    // scale and bias; lane (hi, l32) holds channels 8j + 4hi + 0..3 of a block, of one token
-    const int cw = m0 + wm * MB * 32 + 4 * hi;  // + 32*m + 8*j
-    const int tw = n0 + wn * NB * 32 + l32;     // + 32*n
-    {
-        float sx[NB];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) sx[n] = X8 && tw + 32 * n < a.tokens ? a.x_scale[tw + 32 * n] : 1.0f;
-        const rsrc_t rs = make_rsrc(a.scale, a.scale ? 4u * (unsigned)a.cout : 0u);
-        const rsrc_t rb = make_rsrc(a.bias, a.bias ? 4u * (unsigned)a.cout : 0u);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = cw + 32 * m + 8 * j;
-                const unsigned off = c < a.cout ? 4u * (unsigned)c : kOOB;
-                f32x4 sc = __builtin_bit_cast(f32x4, bload128(rs, off));
-                const f32x4 bi = __builtin_bit_cast(f32x4, bload128(rb, off));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!a.scale) sc[i] = 1.0f;
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        const float z = X8 ? acc[m][n][4 * j + i] * sx[n] : acc[m][n][4 * j + i];
-                        acc[m][n][4 * j + i] = fmaf(z, sc[i], bi[i]);
-                    }
-                }
-            }
-    }
-
+    // 2^-e, e the exponent of a token's largest |v|
+    auto power = [&](float top) {
+        int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
+        e = e < -24 ? -24 : e > 120 ? 120 : e;
+        return __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
+    };
+    // The tile's low-rank values go to LDS as B operands, high and low part:
+    // [16 ranks][part][hi][token] pieces of eight.
+    const int nrs = (a.rank + 15) / 16;
+    auto at = [&](int rs, int part, int half, int t) {
+        unsigned char* b = rs < 4 ? buf0 + rs * 64 * BN : buf1 + (rs - 4) * 64 * BN;
+        return reinterpret_cast<u32x4*>(b + (((part * 2 + half) * BN + t) * 16));
+    };
     if (a.rank) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int token = tw + 32 * n;
+        if (tid < BN && n0 + tid < a.tokens) {
+            const int token = n0 + tid;
             const int id = adapter_of(a, token);
-            const float alpha = id >= 0 && a.lora_alpha ? a.lora_alpha[id] : 1.0f;
-            const float* part = a.part + (long)token * a.rank + 8 * hi;
-            // v of ranks 16*rs + 8*hi + 0..7 of this lane's token
-            auto low_rank = [&](int rs, float (&v)[8]) {
+            if (id >= 0) {
+                const float alpha = a.lora_alpha ? a.lora_alpha[id] : 1.0f;
+                auto eight = [&](int r, float (&v)[8]) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                if (id >= 0 && 16 * rs + 8 * hi < a.rank) {
-                    for (int s = 0; s < a.slices; ++s) {
-                        const float* p = part + (long)s * a.tokens * a.rank + 16 * rs;
+                    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                    for (int sl = 0; sl < a.slices; ++sl) {
+                        const float* p = a.part + ((long)sl * a.tokens + token) * a.rank + r;
                         const f32x4 p0 = *reinterpret_cast<const f32x4*>(p);
                         const f32x4 p1 = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
@@ -223,85 +238,99 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= alpha;
+                };
+                float down = 1.0f;
+                if constexpr (!V16<T>::BF) {
+                    float top = 0.0f;
+                    for (int r = 0; r < a.rank; r += 8) {
+                        float v[8];
+                        eight(r, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+                    }
+                    down = power(top);
+                    down_lds[tid] = down;
                 }
-            };
-            const int nrs = (a.rank + 15) / 16;
-            float down = 1.0f, up = 1.0f;
-            if constexpr (!V16<T>::BF) {
-                // the power of two that brings the token's largest |v| below 2
-                float top = 0.0f;
-                for (int rs = 0; rs < nrs; ++rs) {
-                    float v[8];
-                    low_rank(rs, v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
-                }
-                top = fmaxf(top, __shfl_xor(top, 32));
-                int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
-                e = e < -24 ? -24 : e > 120 ? 120 : e;
-                if (top > 0.0f) {
-                    up = __builtin_bit_cast(float, (unsigned)(127 + e) << 23);
-                    down = __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
-                }
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[m][n][i] *= down;
-            }
-            unsigned long long todo = __ballot(id >= 0) & 0xffffffffull;
-            while (todo) {  // each pass clears at least its first bit
-                const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-                const bool mine = id == d;
-                todo &= ~__ballot(mine);
-                const rsrc_t rbm = make_rsrc(static_cast<const T*>(a.lora_b) + (long)d * a.cout * a.rank,
-                                             (unsigned)a.cout * (unsigned)a.rank * 2u);
-                f32x16 c[MB];
-#pragma unroll
-                for (int m = 0; m < MB; ++m) c[m] = acc[m][n];
-                for (int rs = 0; rs < nrs; ++rs) {
-                    float v[8];
-                    low_rank(rs, v);
+                for (int r = 0; r < 16 * nrs; r += 8) {
                     v8 vh, vl;
+                    float v[8];
+                    if (r < a.rank) {
+                        eight(r, v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float f = v[e] * down;
                         vh[e] = (T)f;
                         vl[e] = __builtin_isfinite((float)vh[e]) ? (T)(f - (float)vh[e]) : (T)0.0f;
                     }
-                    const int r = 16 * rs + 8 * hi;
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        const int ch = m0 + (wm * MB + m) * 32 + l32;
-                        const unsigned off =
-                            ch < a.cout && r < a.rank ? ((unsigned)ch * (unsigned)a.rank + (unsigned)r) * 2u : kOOB;
-                        const u32x4 b = bload128(rbm, off);
-                        c[m] = mma32<T>(b, __builtin_bit_cast(u32x4, vl), c[m]);
-                        c[m] = mma32<T>(b, __builtin_bit_cast(u32x4, vh), c[m]);
-                    }
+                    *at(r >> 4, 0, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vh);
+                    *at(r >> 4, 1, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vl);
                 }
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[m][n][i] = mine ? c[m][i] : acc[m][n][i];
-            }
-            if constexpr (!V16<T>::BF) {
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[m][n][i] *= up;
             }
         }
+        lds_barrier();
     }
 
+    // 32 x 32 blocks one by one; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one token
+    const rsrc_t rs = make_rsrc(a.scale, a.scale ? 4u * (unsigned)a.cout : 0u);
+    const rsrc_t rb = make_rsrc(a.bias, a.bias ? 4u * (unsigned)a.cout : 0u);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-        const int token = tw + 32 * n;
+        const int tt = (wn * NB + n) * 32 + l32, token = n0 + tt;
+        const float sx = X8 && token < a.tokens ? a.x_scale[token] : 1.0f;
+        const int id = a.rank ? adapter_of(a, token) : -1;
+        const unsigned long long ids = __ballot(id >= 0) & 0xffffffffull;
+        float down = 1.0f, up = 1.0f;
+        if constexpr (!V16<T>::BF) {
+            if (id >= 0) {
+                down = down_lds[tt];
+                up = 1.0f / down;  // a power of two: exact
+            }
+        }
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
+        for (int m = 0; m < MB; ++m) {
+            const int cm = m0 + (wm * MB + m) * 32;
+            f32x16 z;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c = cw + 32 * m + 8 * j;
-                if (token < a.tokens && c < a.cout) {
+                const int c = cm + 8 * j + 4 * hi;
+                const unsigned off = c < a.cout ? 4u * (unsigned)c : kOOB;
+                f32x4 sc = __builtin_bit_cast(f32x4, bload128(rs, off));
+                const f32x4 bi = __builtin_bit_cast(f32x4, bload128(rb, off));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!a.scale) sc[i] = 1.0f;
+                    z[4 * j + i] = fmaf(X8 ? acc[m][n][4 * j + i] * sx : acc[m][n][4 * j + i], sc[i], bi[i]);
+                }
+            }
+            unsigned long long todo = ids;
+            while (todo) {  // each pass clears at least its first bit
+                const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+                const bool mine = id == d;
+                todo &= ~__ballot(mine);
+                const rsrc_t rbm = make_rsrc(static_cast<const T*>(a.lora_b) + (long)d * a.cout * a.rank,
+                                             (unsigned)a.cout * (unsigned)a.rank * 2u);
+                const unsigned row = cm + l32 < a.cout ? (unsigned)(cm + l32) * (unsigned)a.rank * 2u : kOOB;
+                f32x16 c;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) c[i] = V16<T>::BF ? z[i] : z[i] * down;
+                for (int r16 = 0; r16 < nrs; ++r16) {
+                    const int r = 16 * r16 + 8 * hi;
+                    const u32x4 b = bload128(rbm, r < a.rank ? row + 2u * (unsigned)r : kOOB);
+                    c = mma32<T>(b, *at(r16, 1, hi, tt), c);
+                    c = mma32<T>(b, *at(r16, 0, hi, tt), c);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[i] = mine ? (V16<T>::BF ? c[i] : c[i] * up) : z[i];
+            }
+            if (token < a.tokens) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = cm + 8 * j + 4 * hi;
+                    if (c >= a.cout) continue;
                     f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
                     if (a.res) {
                         const v4 rv = *reinterpret_cast<const v4*>(static_cast<const T*>(a.res) + (long)token * a.rs + c);
@@ -310,10 +339,12 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
                     }
                     v4 o;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = (T)finish(acc[m][n][4 * j + i], r[i], a.act, a.res_mode);
+                    for (int i = 0; i < 4; ++i) o[i] = (T)finish(z[4 * j + i], r[i], a.act, a.res_mode);
                     *reinterpret_cast<v4*>(static_cast<T*>(a.y) + (long)token * a.ys + c) = o;
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);  // a block at a time: its values are all that is live beside the sums
+        }
     }
 }
 
