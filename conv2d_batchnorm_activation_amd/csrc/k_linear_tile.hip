@@ -3,7 +3,7 @@
 //
 // The weights are the A operand (rows = output channels) and the tokens the B
 // operand (columns = tokens), so a lane's accumulators are channels of one
-// token.  Four waves, two by two, each 32*MB x 32*NB.  A stage is 128 bytes of
+// token.  A stage is 128 bytes of
 // every row of both operands, loaded straight into LDS; the 16-byte pieces of a
 // row are permuted by the row's index as they are fetched, so that the lanes of
 // an operand read (32 rows, the same piece) fall in different banks while every
@@ -37,26 +37,39 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
+// Orders this wave's LDS accesses (which the hardware keeps in order) for the compiler.
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 template <bool X8>
 struct Op {
     typedef typename std::conditional<X8, i32x8, u32x4>::type type;
 };
 
-template <typename T, bool X8, int MB, int NB>
-__global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinArgs a)
+// WM x WN waves, each MB x NB blocks of 32 x 32.
+template <typename T, bool X8, int WM, int WN, int MB, int NB>
+__global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
 {
     typedef typename V16<T>::v8 v8;
     typedef typename V16<T>::v4 v4;
     typedef typename Op<X8>::type op_t;
     constexpr unsigned XB = X8 ? 1 : 2;
-    constexpr int BM = 64 * MB, BN = 64 * NB;
+    constexpr int W = WM * WN, NT = 64 * W;
+    constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
+    constexpr int FM = BM / (8 * W), FN = BN / (8 * W);  // fetches of eight rows a wave, per stage and operand
     constexpr int STEPS = X8 ? 2 : 4;
+    static_assert(BM >= BN && W * 4096 <= (BM + BN) * 128 && MB % 2 == 0, "LDS is used again after the main loop");
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[(BM + BN) * 128];
     __shared__ __attribute__((aligned(1024))) unsigned char buf1[(BM + BN) * 128];
-    __shared__ float down_lds[V16<T>::BF ? 1 : BN];
+    __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
+    __shared__ float sx_lds[X8 ? BN : 1], down_lds[V16<T>::BF ? 1 : BN];
+    __shared__ int id_lds[BN];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave & 1, wn = wave >> 1;
+    const int wm = wave % WM, wn = wave / WM;
     const int hi = lane >> 5, l32 = lane & 31;
 
     // Workgroups go to the XCDs in turn: give each XCD a run of tiles, and runs
@@ -92,18 +105,19 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
         const bool live = (unsigned)st * 128 + piece < cb;
         const unsigned wl = live ? wo : kOOB, xl = live ? xo : kOOB;
 #pragma unroll
-        for (int i = 0; i < 2 * MB; ++i) {
-            const int left = mrows - 8 * wave - 32 * i;
+        for (int i = 0; i < FM; ++i) {
+            const int left = mrows - 8 * wave - 8 * W * i;
             const unsigned n = left <= 0 ? 0u : (unsigned)(left < 8 ? left : 8) * cb - kb;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wt + (long)(32 * i) * cb + kb, n),
-                                                     (lds_void*)(buf + 1024 * (wave + 4 * i)), 16, wl, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wt + (long)(8 * W * i) * cb + kb, n),
+                                                     (lds_void*)(buf + 1024 * (wave + W * i)), 16, wl, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) {
-            const int left = nrows - 8 * wave - 32 * i;
+        for (int i = 0; i < FN; ++i) {
+            const int left = nrows - 8 * wave - 8 * W * i;
             const unsigned n = left <= 0 ? 0u : (unsigned)((left < 8 ? left : 8) - 1) * pitch + cb - kb;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xt + (long)(32 * i) * pitch + kb, n),
-                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + 4 * i)), 16, xl, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xt + (long)(8 * W * i) * pitch + kb, n),
+                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16, xl, 0, 0,
+                                                     0);
         }
     };
     unsigned slot[4];
@@ -128,9 +142,9 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
             }
         };
 #pragma unroll
-        for (int m = 0; m < MB; ++m) A[m] = one(pa + 4096 * m);
-#pragma unroll
         for (int n = 0; n < NB; ++n) B[n] = one(pb + 4096 * n);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) A[m] = one(pa + 4096 * m);
     };
 
     f32x16 acc[MB][NB];
@@ -171,7 +185,7 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
         }
     };
     typedef std::integral_constant<int, 0> no_fetch;
-    typedef std::integral_constant<int, 2 * (MB + NB)> fetch;
+    typedef std::integral_constant<int, FM + FN> fetch;
     auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
 #pragma unroll
         for (int s = 0; s + 1 < STEPS; ++s) {
@@ -191,6 +205,16 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
         mul(A1, B1);
         mix(fetch());
     };
+    for (int i = tid; i < BM; i += NT) {
+        const bool ok = m0 + i < a.cout;
+        sc_lds[i] = !a.scale ? 1.0f : ok ? a.scale[m0 + i] : 0.0f;
+        bi_lds[i] = a.bias && ok ? a.bias[m0 + i] : 0.0f;
+    }
+    for (int i = tid; i < BN; i += NT) {
+        const int token = n0 + i;
+        if (X8) sx_lds[i] = token < a.tokens ? a.x_scale[token] : 0.0f;
+        id_lds[i] = a.rank ? adapter_of(a, token) : -1;
+    }
     // An odd number of stages ends with one of zeros; so do the fetches past the last.
     issue(0, buf0);
     __builtin_amdgcn_s_waitcnt(0);
@@ -204,148 +228,208 @@ __global__ void __launch_bounds__(256, MB * NB >= 16 ? 1 : 2) k_linear_tile(LinA
     __builtin_amdgcn_s_waitcnt(0);  // no fetch is under way when LDS is used again
     lds_barrier();
 
-    // 2^-e, e the exponent of a token's largest |v|
-    auto power = [&](float top) {
-        int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
-        e = e < -24 ? -24 : e > 120 ? 120 : e;
-        return __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
-    };
     // The tile's low-rank values go to LDS as B operands, high and low part:
-    // [16 ranks][part][hi][token] pieces of eight.
+    // [16 ranks][part][hi][token] pieces of eight.  A thread makes a token's.
     const int nrs = (a.rank + 15) / 16;
     auto at = [&](int rs, int part, int half, int t) {
         unsigned char* b = rs < 4 ? buf0 + rs * 64 * BN : buf1 + (rs - 4) * 64 * BN;
         return reinterpret_cast<u32x4*>(b + (((part * 2 + half) * BN + t) * 16));
     };
     if (a.rank) {
-        if (tid < BN && n0 + tid < a.tokens) {
+        if (tid < BN && id_lds[tid] >= 0) {
             const int token = n0 + tid;
-            const int id = adapter_of(a, token);
-            if (id >= 0) {
-                const float alpha = a.lora_alpha ? a.lora_alpha[id] : 1.0f;
-                auto eight = [&](int r, float (&v)[8]) {
+            const float alpha = a.lora_alpha ? a.lora_alpha[id_lds[tid]] : 1.0f;
+            auto eight = [&](int r, float (&v)[8]) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                for (int sl = 0; sl < a.slices; ++sl) {
+                    const float* p = a.part + ((long)sl * a.tokens + token) * a.rank + r;
+                    const f32x4 p0 = *reinterpret_cast<const f32x4*>(p);
+                    const f32x4 p1 = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] += p0[e];
+                        v[4 + e] += p1[e];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= alpha;
+            };
+            float down = 1.0f;
+            if constexpr (!V16<T>::BF) {
+                // 2^-e, e the exponent of the token's largest |v|
+                float top = 0.0f;
+                for (int r = 0; r < a.rank; r += 8) {
+                    float v[8];
+                    eight(r, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+                }
+                int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
+                e = e < -24 ? -24 : e > 120 ? 120 : e;
+                down = __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
+                down_lds[tid] = down;
+            }
+            for (int r = 0; r < 16 * nrs; r += 8) {
+                v8 vh, vl;
+                float v[8];
+                if (r < a.rank) {
+                    eight(r, v);
+                } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                    for (int sl = 0; sl < a.slices; ++sl) {
-                        const float* p = a.part + ((long)sl * a.tokens + token) * a.rank + r;
-                        const f32x4 p0 = *reinterpret_cast<const f32x4*>(p);
-                        const f32x4 p1 = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            v[e] += p0[e];
-                            v[4 + e] += p1[e];
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= alpha;
-                };
-                float down = 1.0f;
-                if constexpr (!V16<T>::BF) {
-                    float top = 0.0f;
-                    for (int r = 0; r < a.rank; r += 8) {
-                        float v[8];
-                        eight(r, v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
-                    }
-                    down = power(top);
-                    down_lds[tid] = down;
                 }
-                for (int r = 0; r < 16 * nrs; r += 8) {
-                    v8 vh, vl;
-                    float v[8];
-                    if (r < a.rank) {
-                        eight(r, v);
-                    } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float f = v[e] * down;
-                        vh[e] = (T)f;
-                        vl[e] = __builtin_isfinite((float)vh[e]) ? (T)(f - (float)vh[e]) : (T)0.0f;
-                    }
-                    *at(r >> 4, 0, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vh);
-                    *at(r >> 4, 1, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vl);
+                for (int e = 0; e < 8; ++e) {
+                    const float f = v[e] * down;
+                    vh[e] = (T)f;
+                    vl[e] = __builtin_isfinite((float)vh[e]) ? (T)(f - (float)vh[e]) : (T)0.0f;
                 }
+                *at(r >> 4, 0, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vh);
+                *at(r >> 4, 1, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vl);
             }
         }
         lds_barrier();
     }
 
-    // 32 x 32 blocks one by one; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one token
-    const rsrc_t rs = make_rsrc(a.scale, a.scale ? 4u * (unsigned)a.cout : 0u);
-    const rsrc_t rb = make_rsrc(a.bias, a.bias ? 4u * (unsigned)a.cout : 0u);
+    // 32 tokens at a time; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one
+    // token.  All that is loaded comes before the first store, which it would
+    // otherwise wait for: finished values are kept, packed, until the end.
+    // Rows past the last token are past the residual's and the output's range.
+    const rsrc_t rres = make_rsrc(static_cast<const T*>(a.res) + (long)n0 * a.rs,
+                                  a.res ? (unsigned)((nrows - 1) * a.rs + a.cout) * 2u : 0u);
+    const rsrc_t ry = make_rsrc(static_cast<T*>(a.y) + (long)n0 * a.ys, (unsigned)((nrows - 1) * a.ys + a.cout) * 2u);
+    v4 out[NB][MB][4];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-        const int tt = (wn * NB + n) * 32 + l32, token = n0 + tt;
-        const float sx = X8 && token < a.tokens ? a.x_scale[token] : 1.0f;
-        const int id = a.rank ? adapter_of(a, token) : -1;
-        const unsigned long long ids = __ballot(id >= 0) & 0xffffffffull;
+        const int t = (wn * NB + n) * 32 + l32;
+        const float sx = X8 ? sx_lds[t] : 1.0f;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = (wm * MB + m) * 32 + 8 * j + 4 * hi;
+                const f32x4 sc = *reinterpret_cast<const f32x4*>(sc_lds + c);
+                const f32x4 bi = *reinterpret_cast<const f32x4*>(bi_lds + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float z = acc[m][n][4 * j + i];
+                    acc[m][n][4 * j + i] = fmaf(X8 ? z * sx : z, sc[i], bi[i]);
+                }
+            }
+
+        const int id = id_lds[t];
+        unsigned long long todo = __ballot(id >= 0) & 0xffffffffull;
         float down = 1.0f, up = 1.0f;
         if constexpr (!V16<T>::BF) {
             if (id >= 0) {
-                down = down_lds[tt];
+                down = down_lds[t];
                 up = 1.0f / down;  // a power of two: exact
             }
         }
+        while (todo) {  // each pass clears at least the first bit
+            const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+            const bool mine = id == d;
+            todo &= ~__ballot(mine);
+            const rsrc_t rbm = make_rsrc(static_cast<const T*>(a.lora_b) + (long)d * a.cout * a.rank,
+                                         (unsigned)a.cout * (unsigned)a.rank * 2u);
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            const int cm = m0 + (wm * MB + m) * 32;
-            f32x16 z;
+            for (int mh = 0; mh < MB; mh += 2) {
+                u32x4 b[2], next[2];
+                unsigned row[2];  // this lane's rows of the adapter's B
+                f32x16 c[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = cm + 8 * j + 4 * hi;
-                const unsigned off = c < a.cout ? 4u * (unsigned)c : kOOB;
-                f32x4 sc = __builtin_bit_cast(f32x4, bload128(rs, off));
-                const f32x4 bi = __builtin_bit_cast(f32x4, bload128(rb, off));
+                for (int m = 0; m < 2; ++m) {
+                    const int ch = m0 + (wm * MB + mh + m) * 32 + l32;
+                    row[m] = ch < a.cout ? (unsigned)ch * (unsigned)a.rank * 2u + 16u * hi : kOOB;
+                    next[m] = bload128(rbm, 8 * hi < a.rank ? row[m] : kOOB);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!a.scale) sc[i] = 1.0f;
-                    z[4 * j + i] = fmaf(X8 ? acc[m][n][4 * j + i] * sx : acc[m][n][4 * j + i], sc[i], bi[i]);
+                    for (int i = 0; i < 16; ++i) c[m][i] = V16<T>::BF ? acc[mh + m][n][i] : acc[mh + m][n][i] * down;
                 }
-            }
-            unsigned long long todo = ids;
-            while (todo) {  // each pass clears at least its first bit
-                const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-                const bool mine = id == d;
-                todo &= ~__ballot(mine);
-                const rsrc_t rbm = make_rsrc(static_cast<const T*>(a.lora_b) + (long)d * a.cout * a.rank,
-                                             (unsigned)a.cout * (unsigned)a.rank * 2u);
-                const unsigned row = cm + l32 < a.cout ? (unsigned)(cm + l32) * (unsigned)a.rank * 2u : kOOB;
-                f32x16 c;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) c[i] = V16<T>::BF ? z[i] : z[i] * down;
                 for (int r16 = 0; r16 < nrs; ++r16) {
-                    const int r = 16 * r16 + 8 * hi;
-                    const u32x4 b = bload128(rbm, r < a.rank ? row + 2u * (unsigned)r : kOOB);
-                    c = mma32<T>(b, *at(r16, 1, hi, tt), c);
-                    c = mma32<T>(b, *at(r16, 0, hi, tt), c);
+                    const u32x4 vl = *at(r16, 1, hi, t), vh = *at(r16, 0, hi, t);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        b[m] = next[m];
+                        next[m] = bload128(rbm, 16 * (r16 + 1) + 8 * hi < a.rank ? row[m] + 32u * (r16 + 1) : kOOB);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[m], vl, c[m]);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[m], vh, c[m]);
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = mine ? (V16<T>::BF ? c[i] : c[i] * up) : z[i];
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[mh + m][n][i] = mine ? (V16<T>::BF ? c[m][i] : c[m][i] * up) : acc[mh + m][n][i];
             }
-            if (token < a.tokens) {
+        }
+
+        __builtin_amdgcn_sched_barrier(0);
+        // residual and activation, each step over all values: one branch a step
+        v4 rv[MB][4];
+        auto add_residual = [&]() {
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][n][4 * j + i] += (float)rv[m][j][i];
+        };
+        if (a.res) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int c = cm + 8 * j + 4 * hi;
-                    if (c >= a.cout) continue;
-                    f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (a.res) {
-                        const v4 rv = *reinterpret_cast<const v4*>(static_cast<const T*>(a.res) + (long)token * a.rs + c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) r[i] = (float)rv[i];
-                    }
-                    v4 o;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = (T)finish(z[4 * j + i], r[i], a.act, a.res_mode);
-                    *reinterpret_cast<v4*>(static_cast<T*>(a.y) + (long)token * a.ys + c) = o;
+                    const int c = m0 + (wm * MB + m) * 32 + 8 * j + 4 * hi;
+                    const unsigned off = c < a.cout ? (unsigned)t * (unsigned)a.rs * 2u + 2u * (unsigned)c : kOOB;
+                    rv[m][j] = __builtin_bit_cast(v4, bload64(rres, off));
                 }
-            }
-            __builtin_amdgcn_sched_barrier(0);  // a block at a time: its values are all that is live beside the sums
+            if (a.res_mode == CVX_RES_BEFORE_ACT) add_residual();
         }
+        if (a.act != CVX_ACT_NONE) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[m][n][i] = apply_act_fast(acc[m][n][i], a.act);
+        }
+        if (a.res_mode == CVX_RES_AFTER_ACT) add_residual();
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[n][m][j][i] = (T)acc[m][n][4 * j + i];
+        __builtin_amdgcn_sched_barrier(0);
     }
+    lds_barrier();  // the low-rank values have been read
+
+    // The output, turned in LDS, 32 tokens x 64 channels at a time: stores of whole lines.
+    unsigned char* turn = buf0 + wave * 4096;
+    const int p = lane & 7;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int m = 0; m < MB; m += 2) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<v4*>(turn + l32 * 128 + ((k ^ (l32 & 7)) * 16) + 8 * hi) = out[n][m + k / 4][k % 4];
+            wave_lds_order();
+            const int c = m0 + (wm * MB + m) * 32 + 8 * p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tt = 8 * i + (lane >> 3), t = (wn * NB + n) * 32 + tt;
+                const u32x4 q = *reinterpret_cast<const u32x4*>(turn + tt * 128 + ((p ^ (tt & 7)) * 16));
+                const unsigned off = ((unsigned)t * (unsigned)a.ys + (unsigned)c) * 2u;
+                const bool live = t < nrows;
+                __builtin_amdgcn_raw_buffer_store_b128(q, ry, live && c + 8 <= a.cout ? (int)off : (int)kOOB, 0, 0);
+                if (a.cout & 4)  // the last four channels of a row
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{q[0], q[1]}, ry,
+                                                          live && c + 4 == a.cout ? (int)off : (int)kOOB, 0, 0);
+            }
+            wave_lds_order();
+        }
 }
 
 template <typename T, bool X8>
@@ -354,12 +438,12 @@ hipError_t launch_tile_t(LinArgs a, const LinPlan& p, hipStream_t s)
     a.tiles_m = (a.cout + 64 * p.mb - 1) / (64 * p.mb);
     a.tiles_n = (a.tokens + 64 * p.nb - 1) / (64 * p.nb);
     const long n = (long)a.tiles_m * a.tiles_n;
-    if (n > (1l << 23)) return hipErrorInvalidValue;  // a grid holds fewer than 2^32 threads
+    if (n > (1l << 22)) return hipErrorInvalidValue;  // a grid holds fewer than 2^32 threads
     const dim3 grid((unsigned)n);
     if (p.mb == 4 && p.nb == 4)
-        hipLaunchKernelGGL((k_linear_tile<T, X8, 4, 4>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_linear_tile<T, X8, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
     else
-        hipLaunchKernelGGL((k_linear_tile<T, X8, 2, 2>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_linear_tile<T, X8, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -402,8 +486,8 @@ void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int 
     if (p.few)
         snprintf(buf, len, "linear few 16x%d%s kernel=cvx::k_linear_few<%s, %s, %d>", 16 * p.nt, lora, t, x8, p.nt);
     else
-        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, %d, %d>", 64 * p.mb, 64 * p.nb, lora,
-                 t, x8, p.mb, p.nb);
+        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, 2, %d, %d, 2>", 64 * p.mb, 64 * p.nb, lora,
+                 t, x8, p.nb, p.mb);
 }
 
 }  // namespace cvx
