@@ -199,7 +199,7 @@ cvx_status cvx_linear(const cvx_linear_desc* d, const void* x, const float* x_sc
     a.slice_chunks = p.slice_chunks;
     a.tiles_m = a.tiles_n = 0;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (lora && launch_lora_down(a, d->dtype, x8, s) != hipSuccess) return CVX_ERR_HIP;
+    if (lora && launch_lora_down(a, p, d->dtype, x8, s) != hipSuccess) return CVX_ERR_HIP;
     const hipError_t e = p.few ? launch_linear_few(a, p, d->dtype, x8, s) : launch_linear_tile(a, p, d->dtype, x8, s);
     return e == hipSuccess ? CVX_OK : CVX_ERR_HIP;
 }

@@ -50,7 +50,7 @@ struct Op {
 };
 
 // WM x WN waves, each MB x NB blocks of 32 x 32.
-template <typename T, bool X8, int WM, int WN, int MB, int NB>
+template <typename T, bool X8, bool LORA, int WM, int WN, int MB, int NB>
 __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
 {
     typedef typename V16<T>::v8 v8;
@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[(BM + BN) * 128];
     __shared__ __attribute__((aligned(1024))) unsigned char buf1[(BM + BN) * 128];
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
-    __shared__ float sx_lds[X8 ? BN : 1], down_lds[V16<T>::BF ? 1 : BN];
-    __shared__ int id_lds[BN];
+    __shared__ float sx_lds[X8 ? BN : 1], down_lds[V16<T>::BF || !LORA ? 1 : BN];
+    __shared__ int id_lds[LORA ? BN : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
     for (int i = tid; i < BN; i += NT) {
         const int token = n0 + i;
         if (X8) sx_lds[i] = token < a.tokens ? a.x_scale[token] : 0.0f;
-        id_lds[i] = a.rank ? adapter_of(a, token) : -1;
+        if (LORA) id_lds[i] = adapter_of(a, token);
     }
     // An odd number of stages ends with one of zeros; so do the fetches past the last.
     issue(0, buf0);
@@ -229,21 +229,24 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
     lds_barrier();
 
     // The tile's low-rank values go to LDS as B operands, high and low part:
-    // [16 ranks][part][hi][token] pieces of eight.  A thread makes a token's.
+    // [16 ranks][part][hi][token] pieces of eight.
     const int nrs = (a.rank + 15) / 16;
     auto at = [&](int rs, int part, int half, int t) {
         unsigned char* b = rs < 4 ? buf0 + rs * 64 * BN : buf1 + (rs - 4) * 64 * BN;
         return reinterpret_cast<u32x4*>(b + (((part * 2 + half) * BN + t) * 16));
     };
-    if (a.rank) {
-        if (tid < BN && id_lds[tid] >= 0) {
-            const int token = n0 + tid;
-            const float alpha = a.lora_alpha ? a.lora_alpha[id_lds[tid]] : 1.0f;
-            auto eight = [&](int r, float (&v)[8]) {
+    if constexpr (LORA) {
+        int lanes = 1;  // lanes that share a token, eight ranks each
+        while (8 * lanes < a.rank) lanes *= 2;
+        const int r = 8 * (tid & (lanes - 1));
+        for (int t = tid / lanes; t < BN; t += NT / lanes) {
+            const int id = id_lds[t];
+            float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            if (id >= 0 && r < a.rank) {
                 for (int sl = 0; sl < a.slices; ++sl) {
-                    const float* p = a.part + ((long)sl * a.tokens + token) * a.rank + r;
+                    const float* p = a.part + ((long)sl * a.tokens + n0 + t) * a.rank + r;
                     const f32x4 p0 = *reinterpret_cast<const f32x4*>(p);
                     const f32x4 p1 = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
@@ -252,50 +255,48 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
                         v[4 + e] += p1[e];
                     }
                 }
+                if (a.lora_alpha) {
+                    const float alpha = a.lora_alpha[id];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= alpha;
-            };
-            float down = 1.0f;
-            if constexpr (!V16<T>::BF) {
-                // 2^-e, e the exponent of the token's largest |v|
-                float top = 0.0f;
-                for (int r = 0; r < a.rank; r += 8) {
-                    float v[8];
-                    eight(r, v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+                    for (int e = 0; e < 8; ++e) v[e] *= alpha;
                 }
+            }
+            if constexpr (!V16<T>::BF) {
+                // times 2^-e, e the exponent of the token's largest |v|
+                float top = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+                for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
                 int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
                 e = e < -24 ? -24 : e > 120 ? 120 : e;
-                down = __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
-                down_lds[tid] = down;
-            }
-            for (int r = 0; r < 16 * nrs; r += 8) {
-                v8 vh, vl;
-                float v[8];
-                if (r < a.rank) {
-                    eight(r, v);
-                } else {
+                const float down = __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
+                if (r == 0) down_lds[t] = down;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                }
+                for (int i = 0; i < 8; ++i) v[i] *= down;
+            }
+            if (r < 16 * nrs) {
+                v8 vh, vl;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float f = v[e] * down;
-                    vh[e] = (T)f;
-                    vl[e] = __builtin_isfinite((float)vh[e]) ? (T)(f - (float)vh[e]) : (T)0.0f;
+                    vh[e] = (T)v[e];
+                    vl[e] = __builtin_isfinite((float)vh[e]) ? (T)(v[e] - (float)vh[e]) : (T)0.0f;
                 }
-                *at(r >> 4, 0, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vh);
-                *at(r >> 4, 1, (r >> 3) & 1, tid) = __builtin_bit_cast(u32x4, vl);
+                *at(r >> 4, 0, (r >> 3) & 1, t) = __builtin_bit_cast(u32x4, vh);
+                *at(r >> 4, 1, (r >> 3) & 1, t) = __builtin_bit_cast(u32x4, vl);
+                if (a.rank == 8) {  // the upper eight of the only sixteen
+                    *at(0, 0, 1, t) = u32x4{0u, 0u, 0u, 0u};
+                    *at(0, 1, 1, t) = u32x4{0u, 0u, 0u, 0u};
+                }
             }
         }
         lds_barrier();
     }
 
     // 32 tokens at a time; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one
-    // token.  All that is loaded comes before the first store, which it would
-    // otherwise wait for: finished values are kept, packed, until the end.
-    // Rows past the last token are past the residual's and the output's range.
+    // token.  A load waits for the stores before it, so finished values are kept,
+    // packed, until all are done; they are turned in LDS, so that a store takes
+    // whole lines.  Rows past the last token are past the residual's and the
+    // output's range.
     const rsrc_t rres = make_rsrc(static_cast<const T*>(a.res) + (long)n0 * a.rs,
                                   a.res ? (unsigned)((nrows - 1) * a.rs + a.cout) * 2u : 0u);
     const rsrc_t ry = make_rsrc(static_cast<T*>(a.y) + (long)n0 * a.ys, (unsigned)((nrows - 1) * a.ys + a.cout) * 2u);
@@ -318,94 +319,101 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
                 }
             }
 
-        const int id = id_lds[t];
-        unsigned long long todo = __ballot(id >= 0) & 0xffffffffull;
-        float down = 1.0f, up = 1.0f;
-        if constexpr (!V16<T>::BF) {
-            if (id >= 0) {
-                down = down_lds[t];
-                up = 1.0f / down;  // a power of two: exact
-            }
-        }
-        while (todo) {  // each pass clears at least the first bit
-            const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-            const bool mine = id == d;
-            todo &= ~__ballot(mine);
-            const rsrc_t rbm = make_rsrc(static_cast<const T*>(a.lora_b) + (long)d * a.cout * a.rank,
-                                         (unsigned)a.cout * (unsigned)a.rank * 2u);
-#pragma unroll
-            for (int mh = 0; mh < MB; mh += 2) {
-                u32x4 b[2], next[2];
-                unsigned row[2];  // this lane's rows of the adapter's B
-                f32x16 c[2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int ch = m0 + (wm * MB + mh + m) * 32 + l32;
-                    row[m] = ch < a.cout ? (unsigned)ch * (unsigned)a.rank * 2u + 16u * hi : kOOB;
-                    next[m] = bload128(rbm, 8 * hi < a.rank ? row[m] : kOOB);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) c[m][i] = V16<T>::BF ? acc[mh + m][n][i] : acc[mh + m][n][i] * down;
+        if constexpr (LORA) {
+            const int id = id_lds[t];
+            unsigned long long todo = __ballot(id >= 0) & 0xffffffffull;
+            float down = 1.0f, up = 1.0f;
+            if constexpr (!V16<T>::BF) {
+                if (id >= 0) {
+                    down = down_lds[t];
+                    up = 1.0f / down;  // a power of two: exact
                 }
-                for (int r16 = 0; r16 < nrs; ++r16) {
-                    const u32x4 vl = *at(r16, 1, hi, t), vh = *at(r16, 0, hi, t);
+            }
+            while (todo) {  // each pass clears at least the first bit
+                const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+                const bool mine = id == d;
+                todo &= ~__ballot(mine);
+                const rsrc_t rbm = make_rsrc(static_cast<const T*>(a.lora_b) + (long)d * a.cout * a.rank,
+                                             (unsigned)a.cout * (unsigned)a.rank * 2u);
+#pragma unroll
+                for (int mh = 0; mh < MB; mh += 2) {
+                    unsigned row[2];  // this lane's rows of the adapter's B
+                    f32x16 c[2];
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        b[m] = next[m];
-                        next[m] = bload128(rbm, 16 * (r16 + 1) + 8 * hi < a.rank ? row[m] + 32u * (r16 + 1) : kOOB);
+                        const int ch = m0 + (wm * MB + mh + m) * 32 + l32;
+                        row[m] = ch < a.cout ? (unsigned)ch * (unsigned)a.rank * 2u + 16u * hi : kOOB;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            c[m][i] = V16<T>::BF ? acc[mh + m][n][i] : acc[mh + m][n][i] * down;
+                    }
+                    for (int r0 = 0; r0 < a.rank; r0 += 32) {
+                        u32x4 b[2][2];
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+                                b[s][m] = bload128(
+                                    rbm, r0 + 16 * s + 8 * hi < a.rank ? row[m] + 2u * (unsigned)(r0 + 16 * s) : kOOB);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+                            if (r0 + 16 * s < a.rank) {
+                                const u32x4 vl = *at(r0 / 16 + s, 1, hi, t), vh = *at(r0 / 16 + s, 0, hi, t);
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[s][m], vl, c[m]);
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[s][m], vh, c[m]);
+                            }
                     }
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[m], vl, c[m]);
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[m], vh, c[m]);
+                        for (int i = 0; i < 16; ++i)
+                            acc[mh + m][n][i] = mine ? (V16<T>::BF ? c[m][i] : c[m][i] * up) : acc[mh + m][n][i];
                 }
+            }
+        }
+
+        // residual and activation, each step over all values: one branch a step
+#pragma unroll
+        for (int mh = 0; mh < MB; mh += 2) {
+            v4 rv[2][4];
+            auto add_residual = [&]() {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[mh + m][n][i] += (float)rv[m][i / 4][i % 4];
+            };
+            auto activate = [&](auto act) {
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[mh + m][n][i] = mine ? (V16<T>::BF ? c[m][i] : c[m][i] * up) : acc[mh + m][n][i];
+                        acc[mh + m][n][i] = apply_act_fast(acc[mh + m][n][i], decltype(act)::value);
+            };
+            if (a.res) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = m0 + (wm * MB + mh + m) * 32 + 8 * j + 4 * hi;
+                        const unsigned off = c < a.cout ? (unsigned)t * (unsigned)a.rs * 2u + 2u * (unsigned)c : kOOB;
+                        rv[m][j] = __builtin_bit_cast(v4, bload64(rres, off));
+                    }
+                if (a.res_mode == CVX_RES_BEFORE_ACT) add_residual();
             }
+            if (a.act == CVX_ACT_RELU) activate(std::integral_constant<int, CVX_ACT_RELU>());
+            if (a.act == CVX_ACT_SILU) activate(std::integral_constant<int, CVX_ACT_SILU>());
+            if (a.res_mode == CVX_RES_AFTER_ACT) add_residual();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) out[n][mh + m][i / 4][i % 4] = (T)acc[mh + m][n][i];
         }
-
-        __builtin_amdgcn_sched_barrier(0);
-        // residual and activation, each step over all values: one branch a step
-        v4 rv[MB][4];
-        auto add_residual = [&]() {
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][n][4 * j + i] += (float)rv[m][j][i];
-        };
-        if (a.res) {
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = m0 + (wm * MB + m) * 32 + 8 * j + 4 * hi;
-                    const unsigned off = c < a.cout ? (unsigned)t * (unsigned)a.rs * 2u + 2u * (unsigned)c : kOOB;
-                    rv[m][j] = __builtin_bit_cast(v4, bload64(rres, off));
-                }
-            if (a.res_mode == CVX_RES_BEFORE_ACT) add_residual();
-        }
-        if (a.act != CVX_ACT_NONE) {
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[m][n][i] = apply_act_fast(acc[m][n][i], a.act);
-        }
-        if (a.res_mode == CVX_RES_AFTER_ACT) add_residual();
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[n][m][j][i] = (T)acc[m][n][4 * j + i];
         __builtin_amdgcn_sched_barrier(0);
     }
-    lds_barrier();  // the low-rank values have been read
+    if (LORA) lds_barrier();  // the low-rank values have been read
 
-    // The output, turned in LDS, 32 tokens x 64 channels at a time: stores of whole lines.
     unsigned char* turn = buf0 + wave * 4096;
     const int p = lane & 7;
 #pragma unroll
@@ -440,10 +448,15 @@ hipError_t launch_tile_t(LinArgs a, const LinPlan& p, hipStream_t s)
     const long n = (long)a.tiles_m * a.tiles_n;
     if (n > (1l << 22)) return hipErrorInvalidValue;  // a grid holds fewer than 2^32 threads
     const dim3 grid((unsigned)n);
-    if (p.mb == 4 && p.nb == 4)
-        hipLaunchKernelGGL((k_linear_tile<T, X8, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
+    const bool big = p.mb == 4;
+    if (big && a.rank)
+        hipLaunchKernelGGL((k_linear_tile<T, X8, true, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
+    else if (big)
+        hipLaunchKernelGGL((k_linear_tile<T, X8, false, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
+    else if (a.rank)
+        hipLaunchKernelGGL((k_linear_tile<T, X8, true, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((k_linear_tile<T, X8, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_linear_tile<T, X8, false, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -462,12 +475,15 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     p.nt = d.tokens <= 16 ? 1 : d.tokens <= 32 ? 2 : 4;
     const long big = (long)((d.c_out + 255) / 256) * ((d.tokens + 255) / 256);
     p.mb = p.nb = big >= 192 ? 4 : 2;
-    p.slices = p.slice_chunks = 0;
+    p.slices = p.slice_chunks = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
     if (d.rank) {
         // slices of c_in until the first product's grid fills the device
         const long chunks = (d.c_in + kLoraChunk - 1) / kLoraChunk;
-        const long blocks = (long)((d.tokens + 15) / 16) * ((d.rank + 15) / 16);
+        p.down_nb = d.tokens <= 64 ? 0 : d.tokens < 2048 ? 1 : 2;
+        p.down_rc = p.down_nb == 2 && d.rank > 16 ? 4 : 1;
+        const int tok = p.down_nb ? 16 * p.down_nb : 1;
+        const long blocks = (long)((d.tokens + tok - 1) / tok) * ((d.rank + 16 * p.down_rc - 1) / (16 * p.down_rc));
         long want = (512 + blocks - 1) / blocks;
         if (want > chunks) want = chunks;
         p.slice_chunks = (int)((chunks + want - 1) / want);
@@ -486,8 +502,8 @@ void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int 
     if (p.few)
         snprintf(buf, len, "linear few 16x%d%s kernel=cvx::k_linear_few<%s, %s, %d>", 16 * p.nt, lora, t, x8, p.nt);
     else
-        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, 2, %d, %d, 2>", 64 * p.mb, 64 * p.nb, lora,
-                 t, x8, p.nb, p.mb);
+        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, %s, 2, %d, %d, 2>", 64 * p.mb, 64 * p.nb, lora,
+                 t, x8, d.rank ? "true" : "false", p.nb, p.mb);
 }
 
 }  // namespace cvx

@@ -2,13 +2,14 @@
 //     v_t[r] = x_scale[t] * sum_i A_d[r][i] * x_t[i],   d = the token's adapter,
 // for tokens of many adapters at once.
 //
-// A wave holds 16 tokens' values of 256 channels in registers as the matrix
-// instruction's B operand, and goes through the distinct adapters of its 16
-// tokens: each adapter's 16 x 256 block of A streams past once, and the lanes
-// (one token each) whose token names that adapter keep the product.  So a block
-// of tokens of one request costs one pass, 16 tokens of 16 requests cost the 16
-// adapters' bytes they cannot do without, and a value of another adapter never
-// enters a token's sum.  The four waves of a workgroup take the four quarters
+// A wave holds 16*NB tokens' values of 256 channels in registers as the matrix
+// instruction's B operands, and goes through the distinct adapters of its tokens:
+// each adapter's 16 x 256 block of A streams past once, and the lanes (one token
+// each) whose token names that adapter keep the product.  So a block of tokens
+// of one request costs one pass, tokens of many requests cost their adapters'
+// bytes, and a value of another adapter never enters a token's sum.  Where there
+// are few tokens, each likely of a request of its own, a block is one token:
+// the passes over adapters are then workgroups side by side.  The four waves of a workgroup take the four quarters
 // of 1024 channels and add their sums in LDS in a fixed order; a workgroup
 // covers `slice_chunks` such steps, and the slices of c_in that make up the
 // grid when there are few tokens are added, in order, by the kernel that reads
@@ -21,89 +22,147 @@ namespace cvx {
 
 namespace {
 
-template <typename T, bool X8>
+// A block is 16*NB tokens, or a single one (NB = 0); a workgroup takes RC times 16 ranks.
+template <typename T, bool X8, int NB, int RC>
 __global__ void __launch_bounds__(256) k_lora_down(LinArgs a)
 {
-    __shared__ f32x4 red[4][64];
+    constexpr int B = NB ? NB : 1, TOK = NB ? 16 * NB : 1;
+    constexpr unsigned XB = X8 ? 1 : 2;  // bytes of an x value
+    __shared__ f32x4 red[4][RC * B][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int t0 = blockIdx.x * 16;
-    const int token = t0 + (lane & 15);
-    const int r0 = blockIdx.z * 16;
-    const int q = lane >> 4;
-    const int id = adapter_of(a, token);
-    constexpr unsigned XB = X8 ? 1 : 2;  // bytes of an x value
-    const int rows = a.tokens - t0 < 16 ? a.tokens - t0 : 16;
+    const int t0 = blockIdx.x * TOK;
+    const int r0 = blockIdx.z * 16 * RC;
+    const int q = lane >> 4, l16 = lane & 15;
+    const int rows = a.tokens - t0 < TOK ? a.tokens - t0 : TOK;
     const rsrc_t rx = make_rsrc(static_cast<const char*>(a.x) + (long)t0 * a.xs * XB,
                                 (unsigned)(((rows - 1) * a.xs + a.cin) * XB));
-    const unsigned xrow = (lane & 15) < rows ? (unsigned)((lane & 15) * a.xs * XB) : kOOB;
-    const int ar = r0 + (lane & 15);  // row of A this lane holds
+    int id[B];
+    unsigned xrow[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        const int t = 16 * b + l16;
+        id[b] = t < rows ? adapter_of(a, t0 + t) : -1;
+        xrow[b] = t < rows ? (unsigned)(t * a.xs * XB) : kOOB;
+    }
 
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 acc[RC][B];
+#pragma unroll
+    for (int r = 0; r < RC; ++r)
+#pragma unroll
+        for (int b = 0; b < B; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int ch = 0; ch < a.slice_chunks; ++ch) {
         const int k0 = (blockIdx.y * a.slice_chunks + ch) * kLoraChunk + wave * 256;
         if (k0 >= a.cin) break;  // later steps are past it too
-        u32x4 xv[8];
+        // the eight channels a lane holds of step s: 16-byte loads of either type
+        auto channel = [&](int s) { return X8 ? k0 + 64 * (s >> 1) + 16 * q + 8 * (s & 1) : k0 + 32 * s + 8 * q; };
+        u32x4 xv[B][8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const int k = k0 + 32 * s + 8 * q;
-            const unsigned off = k < a.cin && xrow != kOOB ? xrow + (unsigned)k * XB : kOOB;
-            if constexpr (X8)
-                xv[s] = widen8<T>(bload64(rx, off));
-            else
-                xv[s] = bload128(rx, off);
+        for (int b = 0; b < B; ++b) {
+            if constexpr (X8) {
+                u32x4 x8[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int k = channel(2 * s);
+                    x8[s] = bload128(rx, k < a.cin && xrow[b] != kOOB ? xrow[b] + (unsigned)k : kOOB);
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    xv[b][2 * s] = widen8<T>(u32x2{x8[s][0], x8[s][1]});
+                    xv[b][2 * s + 1] = widen8<T>(u32x2{x8[s][2], x8[s][3]});
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const int k = channel(s);
+                    xv[b][s] = bload128(rx, k < a.cin && xrow[b] != kOOB ? xrow[b] + (unsigned)k * XB : kOOB);
+                }
+            }
         }
-        unsigned long long todo = __ballot(id >= 0) & 0xffffull;
-        while (todo) {  // each pass clears at least its first bit
-            const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-            const bool mine = id == d;
-            todo &= ~__ballot(mine);
+        unsigned long long todo[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) todo[b] = __ballot(id[b] >= 0) & 0xffffull;
+        for (;;) {  // each pass clears at least one bit
+            int d = -1;
+#pragma unroll
+            for (int b = B - 1; b >= 0; --b)
+                if (todo[b]) d = __builtin_amdgcn_readlane(id[b], __builtin_ctzll(todo[b]));
+            if (d < 0) break;
             const rsrc_t ra = make_rsrc(static_cast<const T*>(a.lora_a) + (long)d * a.rank * a.cin,
                                         (unsigned)a.rank * (unsigned)a.cin * 2u);
-            f32x4 c = acc;
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int k = k0 + 32 * s + 8 * q;
-                const unsigned off = k < a.cin && ar < a.rank ? ((unsigned)ar * (unsigned)a.cin + (unsigned)k) * 2u : kOOB;
-                c = mma16<T>(bload128(ra, off), xv[s], c);
+            for (int r = 0; r < RC; ++r) {
+                const int ar = r0 + 16 * r + l16;  // row of A this lane holds
+                u32x4 av[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const int k = channel(s);
+                    const unsigned off =
+                        k < a.cin && ar < a.rank ? ((unsigned)ar * (unsigned)a.cin + (unsigned)k) * 2u : kOOB;
+                    av[s] = bload128(ra, off);
+                }
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const bool mine = id[b] == d;
+                    if (__ballot(mine) == 0) continue;
+                    f32x4 c = acc[r][b];
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) c = mma16<T>(av[s], xv[b][s], c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][b][i] = mine ? c[i] : acc[r][b][i];
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = mine ? c[i] : acc[i];
+            for (int b = 0; b < B; ++b) todo[b] &= ~__ballot(id[b] == d);
         }
     }
-    red[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-        const f32x4 s0 = red[0][lane], s1 = red[1][lane], s2 = red[2][lane], s3 = red[3][lane];
-        const int r = r0 + 4 * q;
-        if (token < a.tokens && r < a.rank) {
-            const float xs = X8 ? a.x_scale[token] : 1.0f;
-            f32x4 o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = id >= 0 ? xs * (((s0[i] + s1[i]) + s2[i]) + s3[i]) : 0.0f;
-            float* dst = a.part + ((long)blockIdx.y * a.tokens + token) * a.rank + r;
-            *reinterpret_cast<f32x4*>(dst) = o;  // rank is a multiple of 8: whole, aligned vectors
+    for (int r = 0; r < RC; ++r)
+#pragma unroll
+        for (int b = 0; b < B; ++b) red[wave][r * B + b][lane] = acc[r][b];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RC; ++r)
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if ((r * B + b) % 4 != wave) continue;
+            const f32x4 s0 = red[0][r * B + b][lane], s1 = red[1][r * B + b][lane], s2 = red[2][r * B + b][lane],
+                        s3 = red[3][r * B + b][lane];
+            const int t = 16 * b + l16, rank = r0 + 16 * r + 4 * q;
+            if (t < rows && rank < a.rank) {
+                const float xs = X8 ? a.x_scale[t0 + t] : 1.0f;
+                f32x4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = id[b] >= 0 ? xs * (((s0[i] + s1[i]) + s2[i]) + s3[i]) : 0.0f;
+                // rank is a multiple of 8: whole, aligned vectors
+                *reinterpret_cast<f32x4*>(a.part + ((long)blockIdx.y * a.tokens + t0 + t) * a.rank + rank) = o;
+            }
         }
-    }
+}
+
+template <typename T, bool X8>
+hipError_t launch_down_t(const LinArgs& a, const LinPlan& p, hipStream_t s)
+{
+    const int tok = p.down_nb ? 16 * p.down_nb : 1;
+    const dim3 grid((unsigned)((a.tokens + tok - 1) / tok), (unsigned)a.slices,
+                    (unsigned)((a.rank + 16 * p.down_rc - 1) / (16 * p.down_rc)));
+    if (p.down_nb == 0)
+        hipLaunchKernelGGL((k_lora_down<T, X8, 0, 1>), grid, dim3(256), 0, s, a);
+    else if (p.down_nb == 1)
+        hipLaunchKernelGGL((k_lora_down<T, X8, 1, 1>), grid, dim3(256), 0, s, a);
+    else if (p.down_rc == 1)
+        hipLaunchKernelGGL((k_lora_down<T, X8, 2, 1>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_lora_down<T, X8, 2, 4>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_lora_down(const LinArgs& a, int dtype, int x8, hipStream_t s)
+hipError_t launch_lora_down(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.tokens + 15) / 16), (unsigned)a.slices, (unsigned)((a.rank + 15) / 16));
-    if (dtype == CVX_DT_F16) {
-        if (x8)
-            hipLaunchKernelGGL((k_lora_down<half_t, true>), grid, dim3(256), 0, s, a);
-        else
-            hipLaunchKernelGGL((k_lora_down<half_t, false>), grid, dim3(256), 0, s, a);
-    } else {
-        if (x8)
-            hipLaunchKernelGGL((k_lora_down<bf16_t, true>), grid, dim3(256), 0, s, a);
-        else
-            hipLaunchKernelGGL((k_lora_down<bf16_t, false>), grid, dim3(256), 0, s, a);
-    }
-    return hipGetLastError();
+    if (dtype == CVX_DT_F16) return x8 ? launch_down_t<half_t, true>(a, p, s) : launch_down_t<half_t, false>(a, p, s);
+    return x8 ? launch_down_t<bf16_t, true>(a, p, s) : launch_down_t<bf16_t, false>(a, p, s);
 }
 
 }  // namespace cvx

@@ -55,6 +55,7 @@ struct LinPlan {
     int nt;              // few: 16-token blocks a workgroup holds
     int mb, nb;          // tile: 64*mb channels x 64*nb tokens
     int slices, slice_chunks;
+    int down_nb, down_rc;  // first product: 16-token blocks (0: one token) and 16-rank blocks a workgroup
     size_t ws_bytes;
 };
 
@@ -63,7 +64,7 @@ constexpr int kLoraMaxRank = 128;
 
 LinPlan linear_plan(const cvx_linear_desc& d);
 void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int len);
-hipError_t launch_lora_down(const LinArgs& a, int dtype, int x8, hipStream_t s);
+hipError_t launch_lora_down(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s);
 hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s);
 hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s);
 
