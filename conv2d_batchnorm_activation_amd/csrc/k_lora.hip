@@ -31,7 +31,10 @@ __global__ void __launch_bounds__(256) k_lora_down(LinArgs a)
     __shared__ f32x4 red[4][RC * B][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int t0 = blockIdx.x * TOK;
+    // Consecutive blocks of tokens, which share adapters, on one XCD (workgroups go
+    // to the eight in turn), so that its cache holds the adapters of its tokens.
+    const int xcd = blockIdx.x & 7, per = gridDim.x >> 3, rest = gridDim.x & 7;
+    const int t0 = (xcd * per + (xcd < rest ? xcd : rest) + (int)(blockIdx.x >> 3)) * TOK;
     const int r0 = blockIdx.z * 16 * RC;
     const int q = lane >> 4, l16 = lane & 15;
     const int rows = a.tokens - t0 < TOK ? a.tokens - t0 : TOK;
@@ -54,31 +57,18 @@ __global__ void __launch_bounds__(256) k_lora_down(LinArgs a)
     for (int ch = 0; ch < a.slice_chunks; ++ch) {
         const int k0 = (blockIdx.y * a.slice_chunks + ch) * kLoraChunk + wave * 256;
         if (k0 >= a.cin) break;  // later steps are past it too
-        // the eight channels a lane holds of step s: 16-byte loads of either type
-        auto channel = [&](int s) { return X8 ? k0 + 64 * (s >> 1) + 16 * q + 8 * (s & 1) : k0 + 32 * s + 8 * q; };
         u32x4 xv[B][8];
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            if constexpr (X8) {
-                u32x4 x8[4];
+        for (int b = 0; b < B; ++b)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int k = channel(2 * s);
-                    x8[s] = bload128(rx, k < a.cin && xrow[b] != kOOB ? xrow[b] + (unsigned)k : kOOB);
-                }
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    xv[b][2 * s] = widen8<T>(u32x2{x8[s][0], x8[s][1]});
-                    xv[b][2 * s + 1] = widen8<T>(u32x2{x8[s][2], x8[s][3]});
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const int k = channel(s);
-                    xv[b][s] = bload128(rx, k < a.cin && xrow[b] != kOOB ? xrow[b] + (unsigned)k * XB : kOOB);
-                }
+            for (int s = 0; s < 8; ++s) {
+                const int k = k0 + 32 * s + 8 * q;
+                const unsigned off = k < a.cin && xrow[b] != kOOB ? xrow[b] + (unsigned)k * XB : kOOB;
+                if constexpr (X8)
+                    xv[b][s] = widen8<T>(bload64(rx, off));
+                else
+                    xv[b][s] = bload128(rx, off);
             }
-        }
         unsigned long long todo[B];
 #pragma unroll
         for (int b = 0; b < B; ++b) todo[b] = __ballot(id[b] >= 0) & 0xffffull;
@@ -96,7 +86,7 @@ __global__ void __launch_bounds__(256) k_lora_down(LinArgs a)
                 u32x4 av[8];
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
-                    const int k = channel(s);
+                    const int k = k0 + 32 * s + 8 * q;
                     const unsigned off =
                         k < a.cin && ar < a.rank ? ((unsigned)ar * (unsigned)a.cin + (unsigned)k) * 2u : kOOB;
                     av[s] = bload128(ra, off);
