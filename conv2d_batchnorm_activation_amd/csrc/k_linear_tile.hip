@@ -473,6 +473,7 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     LinPlan p;
     p.few = d.tokens <= 64;
     p.nt = d.tokens <= 16 ? 1 : d.tokens <= 32 ? 2 : 4;
+    p.rb = p.nt == 4 && d.c_out >= 32 * 192 ? 2 : 1;
     const long big = (long)((d.c_out + 255) / 256) * ((d.tokens + 255) / 256);
     p.mb = p.nb = big >= 192 ? 4 : 2;
     p.slices = p.slice_chunks = p.down_nb = p.down_rc = 0;
@@ -500,7 +501,8 @@ void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int 
     char lora[64] = "";
     if (d.rank) snprintf(lora, sizeof lora, " rank=%d slices=%d", d.rank, p.slices);
     if (p.few)
-        snprintf(buf, len, "linear few 16x%d%s kernel=cvx::k_linear_few<%s, %s, %d>", 16 * p.nt, lora, t, x8, p.nt);
+        snprintf(buf, len, "linear few %dx%d%s kernel=cvx::k_linear_few<%s, %s, %d, %d, %d, %d, %d>", 16 * p.rb, 16 * p.nt,
+                 lora, t, x8, p.nt == 1 ? 8 : 4, p.rb, p.nt, d.tokens <= 8 ? 8 : 16 * p.nt, p.nt == 4 ? 3 : 4);
     else
         snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, %s, 2, %d, %d, 2>", 64 * p.mb, 64 * p.nb, lora,
                  t, x8, d.rank ? "true" : "false", p.nb, p.mb);

@@ -52,7 +52,7 @@ struct LinArgs {
 // What runs a projection.
 struct LinPlan {
     int few;             // 1: the kernel for few tokens; 0: the tile kernel
-    int nt;              // few: 16-token blocks a workgroup holds
+    int nt, rb;          // few: 16-token blocks and 16-channel blocks a workgroup holds
     int mb, nb;          // tile: 64*mb channels x 64*nb tokens
     int slices, slice_chunks;
     int down_nb, down_rc;  // first product: 16-token blocks (0: one token) and 16-rank blocks a workgroup
