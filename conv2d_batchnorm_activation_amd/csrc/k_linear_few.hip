@@ -84,8 +84,10 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     const int rows = a.cout - c0 < 16 * RB ? a.cout - c0 : 16 * RB;
     const rsrc_t rw = make_rsrc(static_cast<const char*>(a.w) + (long)c0 * cb, (unsigned)rows * cb);
     const rsrc_t rx = make_rsrc(a.x, (unsigned)(a.tokens - 1) * pitch + cb);
-    const unsigned piece = (unsigned)((lane & 7) ^ (lane >> 3)) * 16;
-    const unsigned wo = (unsigned)(lane >> 3) * cb + piece, xo = (unsigned)(lane >> 3) * pitch + piece;
+    // The 16-byte pieces of row r lie permuted, piece p at p ^ (r/2 % 8): the sixteen
+    // lanes of an operand read that go together then fall in all of the banks.
+    const unsigned piece[2] = {(unsigned)((lane & 7) ^ (lane >> 4)) * 16, (unsigned)((lane & 7) ^ (4 + (lane >> 4))) * 16};
+    const unsigned wo = (unsigned)(lane >> 3) * cb, xo = (unsigned)(lane >> 3) * pitch;
 
     // A wave's stages are wave, wave + W, ...; every workgroup begins at another one
     // of them, as rows a power of two apart keep a piece's lines in few channels
@@ -97,16 +99,16 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     auto issue = [&](int i, unsigned char* st) {
         const int j = i + turn < steps ? i + turn : i + turn - steps;
         const unsigned kb = (unsigned)(wave + W * j) * 128;
-        const bool live = i < steps && kb + piece < cb;
+        const bool live[2] = {i < steps && kb + piece[0] < cb, i < steps && kb + piece[1] < cb};
         unsigned char* p = st + wave * SB;
 #pragma unroll
         for (int r = 0; r < 2 * RB; ++r)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(p + 1024 * r), 16,
-                                                     live ? wo + 8 * r * cb + kb : kOOB, 0, 0, 0);
+                                                     live[r & 1] ? wo + 8 * r * cb + kb + piece[r & 1] : kOOB, 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < XR / 8; ++r)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(p + WB + 1024 * r), 16,
-                                                     live ? xo + 8 * r * pitch + kb : kOOB, 0, 0, 0);
+                                                     live[r & 1] ? xo + 8 * r * pitch + kb + piece[r & 1] : kOOB, 0, 0, 0);
     };
     f32x4 acc[RB][NT];
 #pragma unroll
@@ -120,12 +122,13 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
         u32x4 wv[2][RB], xv[2][NT];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const unsigned slot = (unsigned)((4 * s + q) ^ (lane & 7)) * 16;
+            const unsigned slot = (unsigned)((4 * s + q) ^ (l16 >> 1)) * 16;
 #pragma unroll
             for (int r = 0; r < RB; ++r) wv[s][r] = *reinterpret_cast<const u32x4*>(p + 2048 * r + l16 * 128 + slot);
 #pragma unroll
             for (int n = 0; n < NT; ++n)  // eight rows: columns 8 to 15 are of no token
-                xv[s][n] = *reinterpret_cast<const u32x4*>(p + WB + (XR == 8 ? lane & 7 : 16 * n + l16) * 128 + slot);
+                xv[s][n] = *reinterpret_cast<const u32x4*>(p + WB + (XR == 8 ? (lane & 7) * 128 + ((4 * s + q) ^ ((lane & 7) >> 1)) * 16
+                                                                                    : (16 * n + l16) * 128 + slot));
         }
         wait_lds();
         issue(i + D, st);

@@ -26,6 +26,7 @@
 // fp16); the lanes whose token names the adapter keep the result.  fp16, whose
 // range v may leave, takes v and the sums divided by a power of two per token.
 #include <stdio.h>
+#include <stdlib.h>
 
 #include "lin_common.h"
 
@@ -49,9 +50,17 @@ struct Op {
     typedef typename std::conditional<X8, i32x8, u32x4>::type type;
 };
 
-// WM x WN waves, each MB x NB blocks of 32 x 32.
-template <typename T, bool X8, bool LORA, int WM, int WN, int MB, int NB>
-__global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
+// Waits until at most N fetches are under way and what was read from LDS is
+// here; no memory access moves across it.
+template <int N>
+__device__ __forceinline__ void wait_arrived()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// WM x WN waves, each MB x NB blocks of 32 x 32; D stage buffers.
+template <typename T, bool X8, bool LORA, int WM, int WN, int MB, int NB, int D>
+__global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(LinArgs a)
 {
     typedef typename V16<T>::v8 v8;
     typedef typename V16<T>::v4 v4;
@@ -61,9 +70,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
     constexpr int FM = BM / (8 * W), FN = BN / (8 * W);  // fetches of eight rows a wave, per stage and operand
     constexpr int STEPS = X8 ? 2 : 4;
-    static_assert(BM >= BN && W * 4096 <= (BM + BN) * 128 && MB % 2 == 0, "LDS is used again after the main loop");
-    __shared__ __attribute__((aligned(1024))) unsigned char buf0[(BM + BN) * 128];
-    __shared__ __attribute__((aligned(1024))) unsigned char buf1[(BM + BN) * 128];
+    constexpr int SB = (BM + BN) * 128, PER = SB / (64 * BN);  // bytes of a stage, 16-rank values in one
+    static_assert(D == 2 || D == 4, "stage buffers");
+    static_assert(PER * D >= kLoraMaxRank / 16 && W * 4096 <= SB && MB % 2 == 0, "LDS is used again after the main loop");
+    // an array a stage, so that waits are for the stage read, not for every fetch
+    __shared__ __attribute__((aligned(1024))) unsigned char buf0[SB], buf1[SB], buf2[D == 4 ? SB : 16],
+        buf3[D == 4 ? SB : 16];
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
     __shared__ float sx_lds[X8 ? BN : 1], down_lds[V16<T>::BF || !LORA ? 1 : BN];
     __shared__ int id_lds[LORA ? BN : 1];
@@ -90,39 +102,41 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
     const unsigned cb = (unsigned)a.cin * XB, pitch = (unsigned)a.xs * XB;
     const int mrows = a.cout - m0 < BM ? a.cout - m0 : BM;
     const int nrows = a.tokens - n0 < BN ? a.tokens - n0 : BN;
-    const char* wt = static_cast<const char*>(a.w) + (long)(m0 + 8 * wave) * cb;
-    const char* xt = static_cast<const char*>(a.x) + (long)(n0 + 8 * wave) * pitch;
-    const unsigned piece = (unsigned)((lane & 7) ^ (lane >> 3)) * 16;
-    const unsigned wo = (unsigned)(lane >> 3) * cb + piece;
-    const unsigned xo = (unsigned)(lane >> 3) * pitch + piece;
+    const char* wt = static_cast<const char*>(a.w) + (long)m0 * cb;
+    const char* xt = static_cast<const char*>(a.x) + (long)n0 * pitch;
     const int nst = (int)((cb + 127) / 128);
 
-    // Eight rows a fetch.  Each has a descriptor of its own, which ends with the
-    // operand's rows, so what a lane holds is one offset an operand; pieces past
-    // the end of a row are sent out of range.
+    // A fetch is eight rows of 128 bytes, eight lanes a row.  Rows past the operand
+    // are past the range of its descriptor, pieces past the end of a row are sent
+    // there.  The 16-byte pieces of row r lie permuted, piece p at p ^ (r/2 % 8): the
+    // sixteen lanes of an operand read that go together (0-3, 12-15, 20-27 of 32,
+    // or the others) then fall in all of the banks.
+    static_assert(W % 2 == 0, "a wave's fetches begin at rows 8 * wave + 16 * i");
+    const unsigned piece = (unsigned)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+    static_assert(FM <= 8 && FN <= 8, "fetches a wave");
+    unsigned wo[8], xo[8];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) wo[i] = (unsigned)(8 * (wave + W * i) + (lane >> 3)) * cb + piece;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) xo[i] = (unsigned)(8 * (wave + W * i) + (lane >> 3)) * pitch + piece;
     auto issue = [&](int st, unsigned char* buf) {
         const unsigned kb = (unsigned)st * 128 < cb ? (unsigned)st * 128 : 0u;  // past the end: nothing is live
-        const bool live = (unsigned)st * 128 + piece < cb;
-        const unsigned wl = live ? wo : kOOB, xl = live ? xo : kOOB;
+        const unsigned dead = (unsigned)st * 128 + piece < cb ? 0u : kOOB;
+        const char *wk = wt + kb, *xk = xt + kb;
+        const unsigned wleft = (unsigned)mrows * cb - kb, xleft = (unsigned)(nrows - 1) * pitch + cb - kb;
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int left = mrows - 8 * wave - 8 * W * i;
-            const unsigned n = left <= 0 ? 0u : (unsigned)(left < 8 ? left : 8) * cb - kb;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wt + (long)(8 * W * i) * cb + kb, n),
-                                                     (lds_void*)(buf + 1024 * (wave + W * i)), 16, wl, 0, 0, 0);
-        }
+        for (int i = 0; i < FM; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wk, wleft), (lds_void*)(buf + 1024 * (wave + W * i)), 16,
+                                                     wo[i] | dead, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            const int left = nrows - 8 * wave - 8 * W * i;
-            const unsigned n = left <= 0 ? 0u : (unsigned)((left < 8 ? left : 8) - 1) * pitch + cb - kb;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xt + (long)(8 * W * i) * pitch + kb, n),
-                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16, xl, 0, 0,
-                                                     0);
-        }
+        for (int i = 0; i < FN; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xk, xleft),
+                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16,
+                                                     xo[i] | dead, 0, 0, 0);
     };
     unsigned slot[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) slot[s] = (unsigned)(l32 * 128 + (((2 * s + hi) ^ (l32 & 7)) * 16));
+    for (int s = 0; s < 4; ++s) slot[s] = (unsigned)(l32 * 128 + (((2 * s + hi) ^ ((l32 >> 1) & 7)) * 16));
     auto read = [&](const unsigned char* buf, int st, op_t (&A)[MB], op_t (&B)[NB]) {
         const unsigned char* pa = buf + wm * MB * 4096;
         const unsigned char* pb = buf + BM * 128 + wn * NB * 4096;
@@ -154,7 +168,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
-    op_t A0[MB], B0[NB], A1[MB], B1[NB];
     auto mul = [&](const op_t (&A)[MB], const op_t (&B)[NB]) {
 #pragma unroll
         for (int m = 0; m < MB; ++m)
@@ -184,26 +197,19 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
             }
         }
     };
-    typedef std::integral_constant<int, 0> no_fetch;
-    typedef std::integral_constant<int, FM + FN> fetch;
-    auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
+    auto mix_all = [&]() {  // the same for a whole stage
+        constexpr int READS = (X8 ? 2 : 1) * (MB + NB) * STEPS, MUL = MB * NB * STEPS, OTHER = READS + FM + FN;
 #pragma unroll
-        for (int s = 0; s + 1 < STEPS; ++s) {
-            if (s & 1) {
-                read(cur, s + 1, A0, B0);
-                mul(A1, B1);
-            } else {
-                read(cur, s + 1, A1, B1);
-                mul(A0, B0);
+        for (int i = 0; i < MUL; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+#pragma unroll
+            for (int o = i * OTHER / MUL; o < (i + 1) * OTHER / MUL; ++o) {
+                if (o % (OTHER / (FM + FN)) == 0)
+                    __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+                else
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
-            mix(no_fetch());
         }
-        __builtin_amdgcn_s_waitcnt(0);  // the next stage has arrived, this wave has read the current one
-        lds_barrier();
-        issue(st + 2, cur);
-        read(nxt, 0, A0, B0);
-        mul(A1, B1);
-        mix(fetch());
     };
     for (int i = tid; i < BM; i += NT) {
         const bool ok = m0 + i < a.cout;
@@ -215,24 +221,82 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
         if (X8) sx_lds[i] = token < a.tokens ? a.x_scale[token] : 0.0f;
         if (LORA) id_lds[i] = adapter_of(a, token);
     }
-    // An odd number of stages ends with one of zeros; so do the fetches past the last.
-    issue(0, buf0);
-    __builtin_amdgcn_s_waitcnt(0);
-    lds_barrier();
-    issue(1, buf1);
-    read(buf0, 0, A0, B0);
-    for (int st = 0; st < nst; st += 2) {
-        stage(st, buf0, buf1);
-        stage(st + 1, buf1, buf0);
+    // Both loops take D stages; those past the last are zeros, and so are the fetches past it.
+    typedef std::integral_constant<int, FM + FN> fetch;
+    if constexpr (D == 2) {
+        // A step's operands are read under the step before.
+        typedef std::integral_constant<int, 0> no_fetch;
+        op_t A0[MB], B0[NB], A1[MB], B1[NB];
+        auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
+#pragma unroll
+            for (int s = 0; s + 1 < STEPS; ++s) {
+                if (s & 1) {
+                    read(cur, s + 1, A0, B0);
+                    mul(A1, B1);
+                } else {
+                    read(cur, s + 1, A1, B1);
+                    mul(A0, B0);
+                }
+                mix(no_fetch());
+            }
+            wait_arrived<0>();  // the next stage has arrived, this wave has read the current one
+            lds_barrier();
+            issue(st + 2, cur);
+            read(nxt, 0, A0, B0);
+            mul(A1, B1);
+            mix(fetch());
+        };
+        issue(0, buf0);
+        wait_arrived<0>();
+        lds_barrier();
+        issue(1, buf1);
+        read(buf0, 0, A0, B0);
+        for (int st = 0; st < nst; st += 2) {
+            stage(st, buf0, buf1);
+            stage(st + 1, buf1, buf0);
+        }
+    } else {
+        // One wave a SIMD: a stage's operands are all read under the stage before, as
+        // a step's products (four instructions) are shorter than a read takes.
+        op_t A0[STEPS][MB], B0[STEPS][NB], A1[STEPS][MB], B1[STEPS][NB];
+        auto read_all = [&](const unsigned char* buf, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB]) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) read(buf, s, A[s], B[s]);
+        };
+        auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB],
+                         op_t(&An)[STEPS][MB], op_t(&Bn)[STEPS][NB]) {
+            wait_arrived<2 * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
+            lds_barrier();
+            issue(st + 4, cur);
+            read_all(nxt, An, Bn);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) mul(A[s], B[s]);
+            mix_all();
+        };
+        issue(0, buf0);
+        issue(1, buf1);
+        issue(2, buf2);
+        issue(3, buf3);
+        wait_arrived<3 * (FM + FN)>();
+        lds_barrier();
+        read_all(buf0, A0, B0);
+        for (int st = 0; st < nst; st += 4) {
+            stage(st, buf0, buf1, A0, B0, A1, B1);
+            stage(st + 1, buf1, buf2, A1, B1, A0, B0);
+            stage(st + 2, buf2, buf3, A0, B0, A1, B1);
+            stage(st + 3, buf3, buf0, A1, B1, A0, B0);
+        }
     }
-    __builtin_amdgcn_s_waitcnt(0);  // no fetch is under way when LDS is used again
+    wait_arrived<0>();  // no fetch is under way when LDS is used again
     lds_barrier();
 
     // The tile's low-rank values go to LDS as B operands, high and low part:
     // [16 ranks][part][hi][token] pieces of eight.
     const int nrs = (a.rank + 15) / 16;
     auto at = [&](int rs, int part, int half, int t) {
-        unsigned char* b = rs < 4 ? buf0 + rs * 64 * BN : buf1 + (rs - 4) * 64 * BN;
+        unsigned char* b = rs < PER       ? buf0 + rs * 64 * BN
+                           : rs < 2 * PER ? buf1 + (rs - PER) * 64 * BN
+                                          : buf2 + (rs - 2 * PER) * 64 * BN;
         return reinterpret_cast<u32x4*>(b + (((part * 2 + half) * BN + t) * 16));
     };
     if constexpr (LORA) {
@@ -440,6 +504,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) k_linear_tile(LinArgs a)
         }
 }
 
+template <typename T, bool X8, int WM, int WN, int MB, int NB, int D>
+void launch_tile_k(const LinArgs& a, dim3 grid, hipStream_t s)
+{
+    if (a.rank)
+        hipLaunchKernelGGL((k_linear_tile<T, X8, true, WM, WN, MB, NB, D>), grid, dim3(64 * WM * WN), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_linear_tile<T, X8, false, WM, WN, MB, NB, D>), grid, dim3(64 * WM * WN), 0, s, a);
+}
+
 template <typename T, bool X8>
 hipError_t launch_tile_t(LinArgs a, const LinPlan& p, hipStream_t s)
 {
@@ -448,15 +521,12 @@ hipError_t launch_tile_t(LinArgs a, const LinPlan& p, hipStream_t s)
     const long n = (long)a.tiles_m * a.tiles_n;
     if (n > (1l << 22)) return hipErrorInvalidValue;  // a grid holds fewer than 2^32 threads
     const dim3 grid((unsigned)n);
-    const bool big = p.mb == 4;
-    if (big && a.rank)
-        hipLaunchKernelGGL((k_linear_tile<T, X8, true, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
-    else if (big)
-        hipLaunchKernelGGL((k_linear_tile<T, X8, false, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
-    else if (a.rank)
-        hipLaunchKernelGGL((k_linear_tile<T, X8, true, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
+    if (p.mb == 4)
+        launch_tile_k<T, X8, 2, 4, 4, 2, 2>(a, grid, s);
+    else if (p.nb == 2)
+        launch_tile_k<T, X8, 2, 2, 2, 2, 4>(a, grid, s);
     else
-        hipLaunchKernelGGL((k_linear_tile<T, X8, false, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
+        launch_tile_k<T, X8, 2, 2, 2, 1, 4>(a, grid, s);
     return hipGetLastError();
 }
 
@@ -475,7 +545,10 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     p.nt = d.tokens <= 16 ? 1 : d.tokens <= 32 ? 2 : 4;
     p.rb = p.nt == 4 && d.c_out >= 32 * 192 ? 2 : 1;
     const long big = (long)((d.c_out + 255) / 256) * ((d.tokens + 255) / 256);
+    const long mid = (long)((d.c_out + 127) / 128) * ((d.tokens + 127) / 128);
     p.mb = p.nb = big >= 192 ? 4 : 2;
+    if (p.mb == 2 && mid < 192) p.nb = 1;
+    if (const char* e = getenv("LIN_TILE")) { p.mb = atoi(e) / 10; p.nb = atoi(e) % 10; }
     p.slices = p.slice_chunks = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
     if (d.rank) {
@@ -504,8 +577,9 @@ void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int 
         snprintf(buf, len, "linear few %dx%d%s kernel=cvx::k_linear_few<%s, %s, %d, %d, %d, %d, %d>", 16 * p.rb, 16 * p.nt,
                  lora, t, x8, p.nt == 1 ? 8 : 4, p.rb, p.nt, d.tokens <= 8 ? 8 : 16 * p.nt, p.nt == 4 ? 3 : 4);
     else
-        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, %s, 2, %d, %d, 2>", 64 * p.mb, 64 * p.nb, lora,
-                 t, x8, d.rank ? "true" : "false", p.nb, p.mb);
+        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, %s, 2, %d, %d, %d, %d>", 64 * p.mb, 64 * p.nb,
+                 lora, t, x8, d.rank ? "true" : "false", p.mb == 4 ? 4 : 2, p.mb, p.mb == 4 ? 2 : p.nb,
+                 p.mb == 4 ? 2 : 4);
 }
 
 }  // namespace cvx
