@@ -26,7 +26,6 @@
 // fp16); the lanes whose token names the adapter keep the result.  fp16, whose
 // range v may leave, takes v and the sums divided by a power of two per token.
 #include <stdio.h>
-#include <stdlib.h>
 
 #include "lin_common.h"
 
@@ -548,7 +547,6 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     const long mid = (long)((d.c_out + 127) / 128) * ((d.tokens + 127) / 128);
     p.mb = p.nb = big >= 192 ? 4 : 2;
     if (p.mb == 2 && mid < 192) p.nb = 1;
-    if (const char* e = getenv("LIN_TILE")) { p.mb = atoi(e) / 10; p.nb = atoi(e) % 10; }
     p.slices = p.slice_chunks = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
     if (d.rank) {

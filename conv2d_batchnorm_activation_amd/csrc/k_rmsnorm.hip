@@ -55,15 +55,41 @@ __device__ __forceinline__ float to_odd(double v)
     return (float)__builtin_bit_cast(double, b);
 }
 
+// The value of another lane of the same 16 (a DPP control), or of lane L.
+template <int CTRL>
+__device__ __forceinline__ double lane_move(double v)
+{
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = __builtin_amdgcn_mov_dpp((int)b, CTRL, 0xf, 0xf, true);
+    const unsigned hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+template <int L>
+__device__ __forceinline__ double lane_value(double v)
+{
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = __builtin_amdgcn_readlane((int)b, L), hi = __builtin_amdgcn_readlane((int)(b >> 32), L);
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+// op over the 64 lanes of a wave, whole: within 16 lanes by DPP (neighbour, pair,
+// mirrored half, mirrored row: lanes that hold the same value are interchangeable),
+// then the four rows.  A quarter of the latency of six shuffles by way of LDS.
+template <typename OP>
+__device__ __forceinline__ double wave_all(double v, OP op)
+{
+    v = op(v, lane_move<0xb1>(v));
+    v = op(v, lane_move<0x4e>(v));
+    v = op(v, lane_move<0x141>(v));
+    v = op(v, lane_move<0x140>(v));
+    return op(op(lane_value<0>(v), lane_value<16>(v)), op(lane_value<32>(v), lane_value<48>(v)));
+}
+
 // Row sums over TPR threads of `s` and maxima of `m`; every thread gets both.
 template <int TPR, bool MAX>
 __device__ __forceinline__ void row_reduce(double& s, double& m)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        s += __shfl_xor(s, o);
-        if (MAX) m = fmax(m, __shfl_xor(m, o));
-    }
+    s = wave_all(s, [](double a, double b) { return a + b; });
+    if (MAX) m = wave_all(m, [](double a, double b) { return fmax(a, b); });
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
         __shared__ double ls[W];
@@ -84,13 +110,13 @@ __device__ __forceinline__ void row_reduce(double& s, double& m)
 }
 
 template <typename T, int TPR, int NV, bool RES, bool OUT8>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(RmsArgs a)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_rmsnorm(RmsArgs a)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
     constexpr int HOLD = NV > 0 ? NV : 1;
-    // The sum of two fp32 values can take more than fp32, so both are held; of two
-    // 16-bit values their fp32 sum is.
-    constexpr bool TWO = RES && sizeof(T) == 4;
+    // The sum of two fp32 values can take more than fp32: for codes, which are rounded
+    // from h itself, both are held; else, and of two 16-bit values, their fp32 sum is.
+    constexpr bool TWO = RES && OUT8 && sizeof(T) == 4;
     constexpr int HOLD2 = TWO ? HOLD : 1;
     typedef typename Vec<T, VEC>::type V;
     typedef typename Vec<float, 4>::type G4;
@@ -160,24 +186,29 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(RmsArgs a)
         }
     };
 
-    float h[HOLD][VEC], h2[HOLD2][VEC];
+    // gamma is held too where that is a few registers: it is then there when the row's sum is
+    constexpr bool KEEP = NV > 0 && NV <= 2;
+    float h[HOLD][VEC], h2[HOLD2][VEC], gam[KEEP ? NV : 1][VEC];
     double ss = 0.0, top = 0.0;
-    auto add = [&](const float (&hv)[VEC], const float (&hw)[VEC], int v) {
+    auto add = [&](const float (&hv)[VEC], const float (&hw)[VEC], int v, int j) {
         float g[VEC];
-        if constexpr (OUT8) load_gamma(v, g);
+        if constexpr (OUT8 && !KEEP) load_gamma(v, g);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const double d = value(hv[e], hw[e]);
             ss += d * d;
-            if constexpr (OUT8) top = fmax(top, fabs(d * (double)g[e]));
+            if constexpr (OUT8) top = fmax(top, fabs(d * (double)(KEEP ? gam[KEEP ? j : 0][e] : g[e])));
         }
     };
-    // calls f(vector's index, its slot) for every vector of this thread
-    auto each = [&](auto f) {
+    // calls f(vector's index, its slot) for every vector of this thread; with `one`
+    // the scheduler keeps them apart, so that one vector's values are live at a time
+    auto each = [&](auto f, bool one = false) {
         if constexpr (NV > 0) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j) {
                 if (lane + j * TPR < nvec) f(lane + j * TPR, j);
+                if (one && NV > 2) __builtin_amdgcn_sched_barrier(0);
+            }
         } else {
             for (int v = lane; v < nvec; v += TPR) {
                 load_h(v, h[0], h2[0]);
@@ -186,9 +217,19 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(RmsArgs a)
         }
     };
     if constexpr (NV > 0) each([&](int v, int j) { load_h(v, h[j], h2[TWO ? j : 0]); });
-    each([&](int v, int j) { add(h[j], h2[TWO ? j : 0], v); });
+    if constexpr (KEEP) each([&](int v, int j) { load_gamma(v, gam[j]); });
+    each([&](int v, int j) { add(h[j], h2[TWO ? j : 0], v, j); }, true);
     row_reduce<TPR, OUT8>(ss, top);
     const double q = 1.0 / sqrt(ss / (double)c + (double)a.eps);
+
+    // The held values are fp32 again from here: kept from above in 64 bits they would
+    // take twice the registers, and a workgroup of 1024 threads the whole of a unit.
+    if constexpr (NV > 2) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) asm volatile("" : "+v"(h[j][e]));
+    }
 
     double f = q;
     if constexpr (OUT8) {
@@ -198,7 +239,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(RmsArgs a)
     each([&](int v, int j) {
         const int i0 = v * VEC;
         float g[VEC], o[VEC];
-        load_gamma(v, g);
+        if constexpr (KEEP)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g[e] = gam[j][e];
+        else
+            load_gamma(v, g);
         if constexpr (OUT8) {
             unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.ys;
 #pragma unroll
@@ -231,7 +276,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(RmsArgs a)
             for (int e = 0; e < VEC; ++e) o[e] = (float)value(h[j][e], h2[TWO ? j : 0][e]);
             store_t(sum, v, o);
         }
-    });
+    }, true);
 }
 
 template <typename T, int TPR, int NV>
@@ -255,18 +300,25 @@ void launch_one(const RmsArgs& a, hipStream_t s)
 template <typename T>
 hipError_t launch_t(const RmsArgs& a, hipStream_t s)
 {
-    constexpr int VEC = 16 / (int)sizeof(T);
+    constexpr int VEC = 16 / (int)sizeof(T), FEW = 512;
     const long nvec = ((long)a.c + VEC - 1) / VEC;
+    const bool few = a.rows <= FEW;
     if (nvec <= 64)
         launch_one<T, 64, 1>(a, s);
     else if (nvec <= 256)
         launch_one<T, 256, 1>(a, s);
-    else if (nvec <= 512)
+    else if (nvec <= 512 && !few)
         launch_one<T, 256, 2>(a, s);
-    else if (nvec <= 1024)
+    else if (nvec <= 1024 && !few)
         launch_one<T, 256, 4>(a, s);
+    else if (nvec <= 1024)
+        launch_one<T, 1024, 1>(a, s);
+    else if (nvec <= 2048)
+        launch_one<T, 1024, 2>(a, s);
     else if (nvec <= 4096)
         launch_one<T, 1024, 4>(a, s);
+    else if (nvec <= 6144)
+        launch_one<T, 1024, 6>(a, s);
     else
         launch_one<T, 1024, 0>(a, s);
     return hipGetLastError();
