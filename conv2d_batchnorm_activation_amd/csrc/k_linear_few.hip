@@ -21,8 +21,6 @@ namespace cvx {
 
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_void;
-
 // The value of another lane of the same row of 16 (a DPP control).
 template <int CTRL>
 __device__ __forceinline__ float lane_move(float v)

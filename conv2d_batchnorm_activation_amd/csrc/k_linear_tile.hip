@@ -23,8 +23,9 @@
 // second product of the adapters is accumulated onto them by the same matrix
 // instructions: for every 32 tokens, each distinct adapter's rows of B, with v
 // as two 16-bit values (v = high + low, so v keeps 16 bits in bf16 and 21 in
-// fp16); the lanes whose token names the adapter keep the result.  fp16, whose
-// range v may leave, takes v and the sums divided by a power of two per token.
+// fp16; k_lora_join makes them); the lanes whose token names the adapter keep the
+// result.  fp16, whose range v may leave, takes v and the sums divided by a power
+// of two per token.
 #include <stdio.h>
 
 #include "lin_common.h"
@@ -35,7 +36,6 @@ namespace cvx {
 
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_void;
 
 // Orders this wave's LDS accesses (which the hardware keeps in order) for the compiler.
 __device__ __forceinline__ void wave_lds_order()
@@ -49,19 +49,10 @@ struct Op {
     typedef typename std::conditional<X8, i32x8, u32x4>::type type;
 };
 
-// Waits until at most N fetches are under way and what was read from LDS is
-// here; no memory access moves across it.
-template <int N>
-__device__ __forceinline__ void wait_arrived()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
-
 // WM x WN waves, each MB x NB blocks of 32 x 32; D stage buffers.
 template <typename T, bool X8, bool LORA, int WM, int WN, int MB, int NB, int D>
 __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(LinArgs a)
 {
-    typedef typename V16<T>::v8 v8;
     typedef typename V16<T>::v4 v4;
     typedef typename Op<X8>::type op_t;
     constexpr unsigned XB = X8 ? 1 : 2;
@@ -69,14 +60,14 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
     constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
     constexpr int FM = BM / (8 * W), FN = BN / (8 * W);  // fetches of eight rows a wave, per stage and operand
     constexpr int STEPS = X8 ? 2 : 4;
-    constexpr int SB = (BM + BN) * 128, PER = SB / (64 * BN);  // bytes of a stage, 16-rank values in one
+    constexpr int SB = (BM + BN) * 128;  // bytes of a stage
     static_assert(D == 2 || D == 4, "stage buffers");
-    static_assert(PER * D >= kLoraMaxRank / 16 && W * 4096 <= SB && MB % 2 == 0, "LDS is used again after the main loop");
+    static_assert(W * 4096 <= SB && MB % 2 == 0, "LDS is used again after the main loop");
     // an array a stage, so that waits are for the stage read, not for every fetch
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[SB], buf1[SB], buf2[D == 4 ? SB : 16],
         buf3[D == 4 ? SB : 16];
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
-    __shared__ float sx_lds[X8 ? BN : 1], down_lds[V16<T>::BF || !LORA ? 1 : BN];
+    __shared__ float sx_lds[X8 ? BN : 1];
     __shared__ int id_lds[LORA ? BN : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -289,72 +280,6 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
     wait_arrived<0>();  // no fetch is under way when LDS is used again
     lds_barrier();
 
-    // The tile's low-rank values go to LDS as B operands, high and low part:
-    // [16 ranks][part][hi][token] pieces of eight.
-    const int nrs = (a.rank + 15) / 16;
-    auto at = [&](int rs, int part, int half, int t) {
-        unsigned char* b = rs < PER       ? buf0 + rs * 64 * BN
-                           : rs < 2 * PER ? buf1 + (rs - PER) * 64 * BN
-                                          : buf2 + (rs - 2 * PER) * 64 * BN;
-        return reinterpret_cast<u32x4*>(b + (((part * 2 + half) * BN + t) * 16));
-    };
-    if constexpr (LORA) {
-        int lanes = 1;  // lanes that share a token, eight ranks each
-        while (8 * lanes < a.rank) lanes *= 2;
-        const int r = 8 * (tid & (lanes - 1));
-        for (int t = tid / lanes; t < BN; t += NT / lanes) {
-            const int id = id_lds[t];
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-            if (id >= 0 && r < a.rank) {
-                for (int sl = 0; sl < a.slices; ++sl) {
-                    const float* p = a.part + ((long)sl * a.tokens + n0 + t) * a.rank + r;
-                    const f32x4 p0 = *reinterpret_cast<const f32x4*>(p);
-                    const f32x4 p1 = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[e] += p0[e];
-                        v[4 + e] += p1[e];
-                    }
-                }
-                if (a.lora_alpha) {
-                    const float alpha = a.lora_alpha[id];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= alpha;
-                }
-            }
-            if constexpr (!V16<T>::BF) {
-                // times 2^-e, e the exponent of the token's largest |v|
-                float top = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
-                for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
-                int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
-                e = e < -24 ? -24 : e > 120 ? 120 : e;
-                const float down = __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
-                if (r == 0) down_lds[t] = down;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= down;
-            }
-            if (r < 16 * nrs) {
-                v8 vh, vl;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    vh[e] = (T)v[e];
-                    vl[e] = __builtin_isfinite((float)vh[e]) ? (T)(v[e] - (float)vh[e]) : (T)0.0f;
-                }
-                *at(r >> 4, 0, (r >> 3) & 1, t) = __builtin_bit_cast(u32x4, vh);
-                *at(r >> 4, 1, (r >> 3) & 1, t) = __builtin_bit_cast(u32x4, vl);
-                if (a.rank == 8) {  // the upper eight of the only sixteen
-                    *at(0, 0, 1, t) = u32x4{0u, 0u, 0u, 0u};
-                    *at(0, 1, 1, t) = u32x4{0u, 0u, 0u, 0u};
-                }
-            }
-        }
-        lds_barrier();
-    }
-
     // 32 tokens at a time; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one
     // token.  A load waits for the stores before it, so finished values are kept,
     // packed, until all are done; they are turned in LDS, so that a store takes
@@ -385,10 +310,13 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         if constexpr (LORA) {
             const int id = id_lds[t];
             unsigned long long todo = __ballot(id >= 0) & 0xffffffffull;
+            // this lane's pieces of v: [eight ranks][part][token]; past the last token, its
+            const long here = n0 + t < a.tokens ? n0 + t : a.tokens - 1;
+            const u32x4* v = reinterpret_cast<const u32x4*>(a.joined) + (2l * hi * a.tokens + here);
             float down = 1.0f, up = 1.0f;
             if constexpr (!V16<T>::BF) {
                 if (id >= 0) {
-                    down = down_lds[t];
+                    down = a.down[here];
                     up = 1.0f / down;  // a power of two: exact
                 }
             }
@@ -421,7 +349,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
                             if (r0 + 16 * s < a.rank) {
-                                const u32x4 vl = *at(r0 / 16 + s, 1, hi, t), vh = *at(r0 / 16 + s, 0, hi, t);
+                                const u32x4 vh = v[(r0 / 4 + 4l * s) * a.tokens], vl = v[(r0 / 4 + 4l * s + 1) * a.tokens];
 #pragma unroll
                                 for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[s][m], vl, c[m]);
 #pragma unroll
@@ -475,7 +403,6 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         }
         __builtin_amdgcn_sched_barrier(0);
     }
-    if (LORA) lds_barrier();  // the low-rank values have been read
 
     unsigned char* turn = buf0 + wave * 4096;
     const int p = lane & 7;
@@ -547,20 +474,22 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     const long mid = (long)((d.c_out + 127) / 128) * ((d.tokens + 127) / 128);
     p.mb = p.nb = big >= 192 ? 4 : 2;
     if (p.mb == 2 && mid < 192) p.nb = 1;
-    p.slices = p.slice_chunks = p.down_nb = p.down_rc = 0;
+    p.slices = p.slice_len = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
     if (d.rank) {
         // slices of c_in until the first product's grid fills the device
-        const long chunks = (d.c_in + kLoraChunk - 1) / kLoraChunk;
-        p.down_nb = d.tokens <= 64 ? 0 : d.tokens < 2048 ? 1 : 2;
-        p.down_rc = p.down_nb == 2 && d.rank > 16 ? 4 : 1;
-        const int tok = p.down_nb ? 16 * p.down_nb : 1;
+        p.down_nb = d.tokens <= 64 ? 0 : d.tokens < 2048 ? 1 : 4;
+        p.down_rc = p.down_nb < 4 || d.rank <= 16 ? 1 : d.rank <= 32 ? 2 : 4;
+        const int tok = p.down_nb ? 16 * p.down_nb : 1, step = p.down_nb == 4 ? kLoraMany : kLoraChunk;
+        const long chunks = (d.c_in + step - 1) / step;
         const long blocks = (long)((d.tokens + tok - 1) / tok) * ((d.rank + 16 * p.down_rc - 1) / (16 * p.down_rc));
-        long want = (512 + blocks - 1) / blocks;
+        long want = ((p.down_nb == 4 ? 768 : 512) + blocks - 1) / blocks;
         if (want > chunks) want = chunks;
-        p.slice_chunks = (int)((chunks + want - 1) / want);
-        p.slices = (int)((chunks + p.slice_chunks - 1) / p.slice_chunks);
+        const int per = (int)((chunks + want - 1) / want);
+        p.slice_len = per * step;
+        p.slices = (int)((chunks + per - 1) / per);
         p.ws_bytes = (size_t)p.slices * d.tokens * d.rank * sizeof(float);
+        if (!p.few) p.ws_bytes += lora_joined_bytes(d.tokens, d.rank) + (size_t)d.tokens * sizeof(float);
     }
     return p;
 }

@@ -78,6 +78,17 @@ __device__ __forceinline__ u32x4 widen8(u32x2 q)
     return __builtin_bit_cast(u32x4, o);
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Waits until at most N of this wave's vector-memory operations (fetches into LDS
+// among them) are under way and what it read from LDS is here; no memory access
+// moves across it.
+template <int N>
+__device__ __forceinline__ void wait_arrived()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
 // An adapter of this token, or -1.
 __device__ __forceinline__ int adapter_of(const LinArgs& a, int token)
 {
