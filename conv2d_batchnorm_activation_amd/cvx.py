@@ -147,15 +147,20 @@ def _check(st: int, where: str) -> None:
 
 def _ptr(t) -> Optional[int]:
     """Device (or raw) pointer of a tensor / int / None."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
     return t.data_ptr()
 
 
+#: the current stream's handle by device index, without the stream object around it
+#: (which takes longer to make than a small layer takes to run)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if torch.cuda.is_initialized() and _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
@@ -316,7 +321,24 @@ def make_rmsnorm_desc(rows, c, dtype, out_dtype=None, eps=1e-6, x_stride=0, res_
                             sum_stride, y_stride)
 
 
+def _elsewhere(x, call, *args) -> bool:
+    """Operators on tokens run on their input's device: where that is not the current
+    one, makes it current, calls again and says so.  Host tensors are refused."""
+    if not isinstance(x, torch.Tensor):
+        return False
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("tensors have to be on a GPU")
+    if dev == torch.cuda.current_device():
+        return False
+    with torch.cuda.device(dev):
+        call(*args)
+    return True
+
+
 def cvx_rmsnorm(desc: cvx_rmsnorm_desc, x, residual, gamma, sum_out, y, y_scale=None, stream=None) -> None:
+    if _elsewhere(x, cvx_rmsnorm, desc, x, residual, gamma, sum_out, y, y_scale, stream):
+        return
     _check(lib.cvx_rmsnorm(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum_out), _ptr(y),
                            _ptr(y_scale), _stream(stream)), "cvx_rmsnorm")
 
@@ -343,6 +365,9 @@ def cvx_linear(desc: cvx_linear_desc, x, w, y, x_scale=None, scale=None, bias=No
     if ws_bytes is None:
         ws_bytes = 0 if workspace is None or isinstance(workspace, int) else \
             workspace.numel() * workspace.element_size()
+    if _elsewhere(x, cvx_linear, desc, x, w, y, x_scale, scale, bias, residual, lora_a, lora_b, lora_alpha, lora_id,
+                  workspace, ws_bytes, stream):
+        return
     _check(lib.cvx_linear(ctypes.byref(desc), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(scale), _ptr(bias),
                           _ptr(residual), _ptr(lora_a), _ptr(lora_b), _ptr(lora_alpha), _ptr(lora_id), _ptr(y),
                           _ptr(workspace), ws_bytes, _stream(stream)), "cvx_linear")
