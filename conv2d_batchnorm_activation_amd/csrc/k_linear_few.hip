@@ -52,14 +52,16 @@ __device__ __forceinline__ void wait_vm()
 // Waits until this wave's LDS reads have returned.
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// NT blocks of 16 tokens, of which XR rows (a multiple of eight) are loaded.
-template <typename T, bool X8, int W, int RB, int NT, int XR, int D>
+// NT blocks of 16 tokens, of which XR rows (a multiple of eight) are loaded.  ONE:
+// a single token with an adapter of up to 16 ranks; the adapter's A goes along as
+// 16 more rows, in every workgroup, which for one token is less than a launch.
+template <typename T, bool X8, bool ONE, int W, int RB, int NT, int XR, int D>
 __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
 {
     typedef typename V16<T>::v8 v8;
     constexpr unsigned XB = X8 ? 1 : 2;
-    constexpr int PER = 2 * RB + XR / 8;       // fetches of eight rows a stage
-    constexpr int WB = 2048 * RB, SB = 1024 * PER;  // bytes of a wave's stage: weights, all
+    constexpr int PER = 2 * RB + XR / 8 + (ONE ? 2 : 0);  // fetches of eight rows a stage
+    constexpr int WB = 2048 * RB, AB = WB + 128 * XR, SB = 1024 * PER;  // a wave's stage: weights, x, A; bytes
     static_assert(D == 3 || D == 4, "stages under way");
     // an array a stage, so that waits are for the stage read, not for every fetch
     __shared__ __attribute__((aligned(1024))) unsigned char st0[W * SB], st1[W * SB], st2[W * SB],
@@ -72,7 +74,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     __shared__ int id_lds[16 * NT];
     __shared__ float alpha_lds[16 * NT];
     const bool beside = a.tokens * a.rank <= BESIDE;
-    float* vlds = beside ? vbeside : reinterpret_cast<float*>(st1);
+    float* vlds = ONE || beside ? vbeside : reinterpret_cast<float*>(st1);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c0 = blockIdx.x * 16 * RB;
@@ -86,6 +88,11 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     // lanes of an operand read that go together then fall in all of the banks.
     const unsigned piece[2] = {(unsigned)((lane & 7) ^ (lane >> 4)) * 16, (unsigned)((lane & 7) ^ (4 + (lane >> 4))) * 16};
     const unsigned wo = (unsigned)(lane >> 3) * cb, xo = (unsigned)(lane >> 3) * pitch;
+
+    // ONE: the token's adapter, whose rows end with its ranks (with none, at once)
+    const int one = ONE ? adapter_of(a, 0) : -1;
+    const rsrc_t ra = make_rsrc(static_cast<const T*>(a.lora_a) + (long)(one < 0 ? 0 : one) * a.rank * a.cin,
+                                one < 0 ? 0u : (unsigned)a.rank * cb);
 
     // A wave's stages are wave, wave + W, ...; every workgroup begins at another one
     // of them, as rows a power of two apart keep a piece's lines in few channels
@@ -107,17 +114,24 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
         for (int r = 0; r < XR / 8; ++r)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(p + WB + 1024 * r), 16,
                                                      live[r & 1] ? xo + 8 * r * pitch + kb + piece[r & 1] : kOOB, 0, 0, 0);
+        if constexpr (ONE)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(p + AB + 1024 * r), 16,
+                                                         live[r & 1] ? wo + 8 * r * cb + kb + piece[r & 1] : kOOB, 0, 0,
+                                                         0);
     };
     f32x4 acc[RB][NT];
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 low = {0.0f, 0.0f, 0.0f, 0.0f};
     // One stage: its operands to registers, its buffer to the stage D on, the products.
     auto stage = [&](int i, unsigned char* st) {
         wait_vm<(D - 1) * PER>();
         const unsigned char* p = st + wave * SB;
-        u32x4 wv[2][RB], xv[2][NT];
+        u32x4 wv[2][RB], xv[2][NT], av[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const unsigned slot = (unsigned)((4 * s + q) ^ (l16 >> 1)) * 16;
@@ -127,6 +141,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
             for (int n = 0; n < NT; ++n)  // eight rows: columns 8 to 15 are of no token
                 xv[s][n] = *reinterpret_cast<const u32x4*>(p + WB + (XR == 8 ? (lane & 7) * 128 + ((4 * s + q) ^ ((lane & 7) >> 1)) * 16
                                                                                     : (16 * n + l16) * 128 + slot));
+            if constexpr (ONE) av[s] = *reinterpret_cast<const u32x4*>(p + AB + l16 * 128 + slot);
         }
         wait_lds();
         issue(i + D, st);
@@ -136,6 +151,9 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
             for (int r = 0; r < RB; ++r)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[r][n] = mma_piece<T, X8>(wv[s][r], xv[s][n], acc[r][n]);
+        if constexpr (ONE)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) low = mma16<T>(av[s], xv[s][0], low);
     };
     auto low_rank = [&]() {  // slices added in order, times the adapter's factor; four ranks a step
         const int total = a.tokens * a.rank;
@@ -183,7 +201,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
             alpha_lds[tid] = d >= 0 && a.lora_alpha ? a.lora_alpha[d] : 1.0f;
         }
         lds_barrier();
-        if (beside) low_rank();
+        if (!ONE && beside) low_rank();
     }
     // The low-rank term.  Lanes take the adapters' rows as they lie in memory, eight
     // ranks each, the first EARLY of a lane's pieces now; the `lanes` of a channel
@@ -230,7 +248,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no fetch is under way when the stages are used again
     __syncthreads();
-    if (a.rank && !beside) low_rank();
+    if (!ONE && a.rank && !beside) low_rank();
     f32x4* red = reinterpret_cast<f32x4*>(st0);  // [wave][RB][NT][lane]
     static_assert(RB * NT * 1024 <= SB, "the sums fit a wave's stage");
     const float* redf = reinterpret_cast<const float*>(st0);
@@ -238,6 +256,18 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     for (int r = 0; r < RB; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) red[((wave * RB + r) * NT + n) * 64 + lane] = acc[r][n];
+    if constexpr (ONE) {
+        // rank r of the token: row r, column 0
+        float* lows = reinterpret_cast<float*>(st1);
+        if (l16 == 0) *reinterpret_cast<f32x4*>(lows + 16 * wave + 4 * q) = low;
+        __syncthreads();
+        if (tid < 16) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) v += lows[16 * w + tid];
+            vlds[tid] = v * alpha_lds[0];
+        }
+    }
     __syncthreads();
     if (a.rank) {
 #pragma unroll
@@ -265,16 +295,22 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     }
 }
 
-template <typename T, bool X8, int W, int RB, int NT, int XR, int D>
+template <typename T, bool X8, int W, int RB, int NT, int XR, int D, bool ONE = false>
 void launch_few_k(const LinArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_linear_few<T, X8, W, RB, NT, XR, D>), dim3((unsigned)((a.cout + 16 * RB - 1) / (16 * RB))),
+    hipLaunchKernelGGL((k_linear_few<T, X8, ONE, W, RB, NT, XR, D>), dim3((unsigned)((a.cout + 16 * RB - 1) / (16 * RB))),
                        dim3(64 * W), 0, s, a);
 }
 
 template <typename T, bool X8>
 hipError_t launch_few_t(const LinArgs& a, const LinPlan& p, hipStream_t s)
 {
+    if constexpr (!X8) {
+        if (p.one) {
+            launch_few_k<T, X8, 8, 1, 1, 8, 3, true>(a, s);
+            return hipGetLastError();
+        }
+    }
     if (a.tokens <= 8)
         launch_few_k<T, X8, 8, 1, 1, 8, 4>(a, s);
     else if (p.nt == 1)

@@ -468,6 +468,7 @@ LinPlan linear_plan(const cvx_linear_desc& d)
 {
     LinPlan p;
     p.few = d.tokens <= 64;
+    p.one = d.tokens == 1 && d.rank > 0 && d.rank <= 16 && d.x_dtype == d.dtype;
     p.nt = d.tokens <= 16 ? 1 : d.tokens <= 32 ? 2 : 4;
     p.rb = p.nt == 4 && d.c_out >= 32 * 192 ? 2 : 1;
     const long big = (long)((d.c_out + 255) / 256) * ((d.tokens + 255) / 256);
@@ -476,7 +477,7 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     if (p.mb == 2 && mid < 192) p.nb = 1;
     p.slices = p.slice_len = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
-    if (d.rank) {
+    if (d.rank && !p.one) {
         // slices of c_in until the first product's grid fills the device
         p.down_nb = d.tokens <= 64 ? 0 : d.tokens < 2048 ? 1 : 4;
         p.down_rc = p.down_nb < 4 || d.rank <= 16 ? 1 : d.rank <= 32 ? 2 : 4;
@@ -499,10 +500,14 @@ void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int 
     const char* t = d.dtype == CVX_DT_F16 ? "_Float16" : "__bf16";
     const char* x8 = d.x_dtype == CVX_DT_E4M3 ? "true" : "false";
     char lora[64] = "";
-    if (d.rank) snprintf(lora, sizeof lora, " rank=%d slices=%d", d.rank, p.slices);
+    if (p.one)
+        snprintf(lora, sizeof lora, " rank=%d", d.rank);
+    else if (d.rank)
+        snprintf(lora, sizeof lora, " rank=%d slices=%d", d.rank, p.slices);
     if (p.few)
-        snprintf(buf, len, "linear few %dx%d%s kernel=cvx::k_linear_few<%s, %s, %d, %d, %d, %d, %d>", 16 * p.rb, 16 * p.nt,
-                 lora, t, x8, p.nt == 1 ? 8 : 4, p.rb, p.nt, d.tokens <= 8 ? 8 : 16 * p.nt, p.nt == 4 ? 3 : 4);
+        snprintf(buf, len, "linear few %dx%d%s kernel=cvx::k_linear_few<%s, %s, %s, %d, %d, %d, %d, %d>", 16 * p.rb,
+                 16 * p.nt, lora, t, x8, p.one ? "true" : "false", p.nt == 1 ? 8 : 4, p.rb, p.nt,
+                 d.tokens <= 8 ? 8 : 16 * p.nt, p.nt == 4 || p.one ? 3 : 4);
     else
         snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, %s, 2, %d, %d, %d, %d>", 64 * p.mb, 64 * p.nb,
                  lora, t, x8, d.rank ? "true" : "false", p.mb == 4 ? 4 : 2, p.mb, p.mb == 4 ? 2 : p.nb,

@@ -189,6 +189,23 @@ def test_linear_adapter_ids(t, ids):
     Case(t, t, 272, 140, (F16, BF16)[t % 2], False, 16, 6, ids=ids, alpha=ids != "one").check()
 
 
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("rank", [8, 16, 24])
+@pytest.mark.parametrize("ci,co", [(8, 4), (1000, 60), (4096, 132)])
+def test_linear_one_token(ci, co, rank, dt):
+    for ids in ("one", "none"):
+        Case(ci + rank, 1, ci, co, dt, False, rank, 3, SILU, 2, ids=ids).check()
+    Case(ci, 1, ci, co, dt, False, rank, 1, ids="one", alpha=False, scale=False, bias=False).check()
+
+
+@pytest.mark.parametrize("x8", [False, True], ids=["x16", "x8"])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("rank", [8, 24, 64, 72, 128])
+def test_linear_adapters_of_prompts(rank, dt, x8):
+    # runs of requests in blocks of 64 tokens, slices of c_in, ranks that fill part of a block
+    Case(rank, 2070, 1168, 68, dt, x8, rank, 7, ids="runs").check()
+
+
 @pytest.mark.parametrize("t", [3, 40, 140])
 @pytest.mark.parametrize("act", [NONE, RELU, SILU])
 @pytest.mark.parametrize("res", [0, 1, 2])

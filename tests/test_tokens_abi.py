@@ -97,7 +97,10 @@ def test_linear_null_descriptor():
 def test_linear_queries():
     assert cvx.cvx_linear_workspace_bytes(lin_desc()) == 0
     assert cvx.cvx_linear_workspace_bytes(lin_desc(c_in=60)) == 0
-    for t in (1, 17, 64, 65, 300, 5000):
+    # one token takes up to 16 ranks in the projection's own kernel
+    assert cvx.cvx_linear_workspace_bytes(lin_desc(tokens=1, rank=16, n_adapters=3)) == 0
+    assert cvx.cvx_linear_workspace_bytes(lin_desc(tokens=1, rank=24, n_adapters=3)) > 0
+    for t in (2, 17, 64, 65, 300, 5000):
         d = lin_desc(tokens=t, c_in=4096, rank=16, n_adapters=3)
         need = cvx.cvx_linear_workspace_bytes(d)
         assert need >= 4 * t * 16
@@ -114,3 +117,12 @@ def test_older_calls_do_not_take_8_bits():
     d = cvx.make_desc(1, 64, 8, 8, 64, 1, 1, 0)
     assert cvx.cvx_nhwc_packed_weights_bytes(d, E4M3) == 0
     assert cvx.lib.cvx_conv_bn_act_nhwc(ctypes.byref(d), E4M3, X, W, SC, BI, None, Y, None) == ARG
+
+
+def test_host_tensors_are_refused():
+    import torch
+    t = torch.zeros(8, 64)
+    with pytest.raises(ValueError):
+        cvx.cvx_rmsnorm(cvx.make_rmsnorm_desc(8, 64, F32), t, None, t[0], None, t.clone())
+    with pytest.raises(ValueError):
+        cvx.cvx_linear(lin_desc(tokens=8, c_out=64), t, t, t.clone())
