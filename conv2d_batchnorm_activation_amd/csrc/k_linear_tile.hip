@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
                 mix(no_fetch());
             }
             wait_arrived<0>();  // the next stage has arrived, this wave has read the current one
-            lds_barrier();
+            stage_barrier();
             issue(st + 2, cur);
             read(nxt, 0, A0, B0);
             mul(A1, B1);
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         };
         issue(0, buf0);
         wait_arrived<0>();
-        lds_barrier();
+        stage_barrier();
         issue(1, buf1);
         read(buf0, 0, A0, B0);
         for (int st = 0; st < nst; st += 2) {
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB],
                          op_t(&An)[STEPS][MB], op_t(&Bn)[STEPS][NB]) {
             wait_arrived<2 * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
-            lds_barrier();
+            stage_barrier();
             issue(st + 4, cur);
             read_all(nxt, An, Bn);
 #pragma unroll
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         issue(2, buf2);
         issue(3, buf3);
         wait_arrived<3 * (FM + FN)>();
-        lds_barrier();
+        stage_barrier();
         read_all(buf0, A0, B0);
         for (int st = 0; st < nst; st += 4) {
             stage(st, buf0, buf1, A0, B0, A1, B1);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         }
     }
     wait_arrived<0>();  // no fetch is under way when LDS is used again
-    lds_barrier();
+    stage_barrier();
 
     // 32 tokens at a time; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one
     // token.  A load waits for the stores before it, so finished values are kept,

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(256) k_lora_down_many(LinArgs a)
         const bool any = __ballot(id == d) != 0;
         auto stage = [&](int st, unsigned char* buf) {
             wait_arrived<F>();
-            lds_barrier();
+            stage_barrier();
             const unsigned char* px = buf + (16 * wave + l16) * 128;
             const unsigned char* pa = buf + 8192;
             const unsigned key = (unsigned)(l16 >> 1);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256) k_lora_down_many(LinArgs a)
                                                                (piece ^ (int)key) * 16);
                 }
             wait_arrived<63>();
-            lds_barrier();  // every wave has read the stage
+            stage_barrier();  // every wave has read the stage
             issue(st + 2, buf, ra);
             if (any) {
 #pragma unroll
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(256) k_lora_down_many(LinArgs a)
             stage(st + 1, buf1);
         }
         wait_arrived<0>();  // no fetch of this adapter is under way when the next one's begin
-        lds_barrier();
+        stage_barrier();
         if (id == d) {
             const float xs = X8 ? a.x_scale[token] : 1.0f;
 #pragma unroll

@@ -89,6 +89,10 @@ __device__ __forceinline__ void wait_arrived()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
+// A barrier that waits for nothing: a wave waits before it for what the others may
+// rely on (wait_arrived).  A fence here would wait for every fetch under way.
+__device__ __forceinline__ void stage_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
 // An adapter of this token, or -1.
 __device__ __forceinline__ int adapter_of(const LinArgs& a, int token)
 {
