@@ -471,10 +471,24 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     p.one = d.tokens == 1 && d.rank > 0 && d.rank <= 16 && d.x_dtype == d.dtype;
     p.nt = d.tokens <= 16 ? 1 : d.tokens <= 32 ? 2 : 4;
     p.rb = p.nt == 4 && d.c_out >= 32 * 192 ? 2 : 1;
-    const long big = (long)((d.c_out + 255) / 256) * ((d.tokens + 255) / 256);
-    const long mid = (long)((d.c_out + 127) / 128) * ((d.tokens + 127) / 128);
-    p.mb = p.nb = big >= 192 ? 4 : 2;
-    if (p.mb == 2 && mid < 192) p.nb = 1;
+    // The tile that ends first by what a stage (128 bytes of every row) and the rest
+    // of a tile measured, in 10 ns, with the tiles one a compute unit.  4096 -> 4096
+    // channels, bf16: 512 tokens 22 us as 128x64 (256 tiles; 31 as 128x128), 1024
+    // tokens 32 us as 128x128 (256 tiles; 44 as 128x64), 4096 tokens 105 us as
+    // 256x256 (256 tiles; 130 as 128x128).
+    const struct {
+        int mb, nb, stage, rest;
+    } tiles[] = {{4, 4, 150, 1000}, {2, 2, 45, 500}, {2, 1, 28, 400}};
+    const long stages = ((long)d.c_in * (d.x_dtype == CVX_DT_E4M3 ? 1 : 2) + 127) / 128;
+    long best = -1;
+    for (const auto& t : tiles) {
+        const long n = (long)((d.c_out + 64 * t.mb - 1) / (64 * t.mb)) * ((d.tokens + 64 * t.nb - 1) / (64 * t.nb));
+        const long time = (n + 255) / 256 * (stages * t.stage + t.rest);
+        if (best >= 0 && time >= best) continue;
+        best = time;
+        p.mb = t.mb;
+        p.nb = t.nb;
+    }
     p.slices = p.slice_len = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
     if (d.rank && !p.one) {
