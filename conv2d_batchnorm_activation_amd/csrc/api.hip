@@ -531,8 +531,8 @@ const char* cvx_status_str(cvx_status s)
     case CVX_OK: return "ok";
     case CVX_ERR_NULL: return "a required pointer is NULL";
     case CVX_ERR_SHAPE: return "sizes are non-positive, inconsistent or too large";
-    case CVX_ERR_UNSUPPORTED: return "convolution not implemented by this library";
-    case CVX_ERR_ALIGN: return "a tensor pointer is not 4-byte aligned";
+    case CVX_ERR_UNSUPPORTED: return "shape or combination not implemented by this library";
+    case CVX_ERR_ALIGN: return "a tensor pointer is not aligned as its call asks";
     case CVX_ERR_ALIAS: return "the output overlaps an input";
     case CVX_ERR_WORKSPACE: return "workspace missing or too small";
     case CVX_ERR_HIP: return "HIP runtime error on launch";

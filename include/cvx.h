@@ -38,8 +38,8 @@ enum {
     CVX_OK = 0,
     CVX_ERR_NULL = -1,        /* a required pointer is NULL                        */
     CVX_ERR_SHAPE = -2,       /* sizes are non-positive, inconsistent or too large */
-    CVX_ERR_UNSUPPORTED = -3, /* valid convolution this library does not implement */
-    CVX_ERR_ALIGN = -4,       /* a tensor pointer is not 4-byte aligned            */
+    CVX_ERR_UNSUPPORTED = -3, /* valid, but not implemented by this library        */
+    CVX_ERR_ALIGN = -4,       /* a tensor pointer is not aligned as its call asks   */
     CVX_ERR_ALIAS = -5,       /* the output overlaps an input                      */
     CVX_ERR_WORKSPACE = -6,   /* workspace NULL or smaller than required           */
     CVX_ERR_HIP = -7,         /* the HIP runtime reported an error on launch       */
