@@ -14,6 +14,7 @@ namespace {
 constexpr long kMaxSpan = 1L << 40;    // elements from an operand's first to its last
 constexpr long kMaxPitch = 1L << 21;   // row stride of a projection's operands: 256 rows stay below 2^31 bytes
 constexpr int kMaxChannels = 1 << 20;  // channels of a projection
+constexpr int kMaxNormed = 1 << 30;    // channels of a row that is normed: their index stays an int
 constexpr int kMaxTokens = 1 << 24;    // tokens of a projection
 
 inline bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -79,7 +80,7 @@ cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc* d, const void* x, const void* res
     if (d->dtype != CVX_DT_F32 && !dtype16(d->dtype)) return CVX_ERR_ARG;
     if (d->out_dtype != d->dtype && d->out_dtype != CVX_DT_E4M3) return CVX_ERR_ARG;
     if (!(d->eps > 0.0f)) return CVX_ERR_ARG;
-    if (d->rows < 1 || d->c < 1) return CVX_ERR_SHAPE;
+    if (d->rows < 1 || d->c < 1 || d->c > kMaxNormed) return CVX_ERR_SHAPE;
     const bool out8 = d->out_dtype == CVX_DT_E4M3;
     RmsArgs a;
     a.rs = a.ss = d->c;

@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_rmsnorm(RmsArgs a)
     double f = q;
     if constexpr (OUT8) {
         f = top > 0.0 ? (double)kE4m3Max / top : 0.0;
-        if (lane == 0) a.y_scale[row] = (float)(top * q / (double)kE4m3Max);
+        // an infinity's row (q = 0) has a NaN scale, also where gamma hides it from `top`
+        if (lane == 0) a.y_scale[row] = q > 0.0 ? (float)(top * q / (double)kE4m3Max) : __builtin_nanf("");
     }
     each([&](int v, int j) {
         const int i0 = v * VEC;
@@ -300,9 +301,14 @@ void launch_one(const RmsArgs& a, hipStream_t s)
 template <typename T>
 hipError_t launch_t(const RmsArgs& a, hipStream_t s)
 {
-    constexpr int VEC = 16 / (int)sizeof(T), FEW = 512;
+    // A row of some hundred vectors is 256 threads' where the rows fill the device, and
+    // 1024 threads' (fewer loads one after another) where they do not.  bf16 with a
+    // residual: 4096 channels, 1 row 2.3 us by 1024 threads, 2.5 by 256; 64 rows 3.3 and
+    // 3.6; 512 rows 5.7 and 5.3; 2048 rows 15.3 and 13.0.  8192 channels: 256 rows 4.9
+    // and 5.7, 512 rows 8.2 and 8.5, 1024 rows 14.2 and 12.5.
+    constexpr int VEC = 16 / (int)sizeof(T);
     const long nvec = ((long)a.c + VEC - 1) / VEC;
-    const bool few = a.rows <= FEW;
+    const bool few = a.rows <= (nvec <= 512 ? 256 : 512);
     if (nvec <= 64)
         launch_one<T, 64, 1>(a, s);
     else if (nvec <= 256)

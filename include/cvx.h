@@ -351,7 +351,7 @@ CVX_API cvx_status cvx_conv_bn_act_nhwc(const cvx_conv_desc *d, int dtype, const
 enum { CVX_DT_E4M3 = 3 };
 
 typedef struct cvx_rmsnorm_desc {
-    int rows, c;        /* x [rows][c]; both at least 1                          */
+    int rows, c;        /* x [rows][c]; both at least 1, c at most 2^30          */
     int dtype;          /* CVX_DT_F32, _F16 or _BF16: x, residual, sum           */
     int out_dtype;      /* type of y: dtype, or CVX_DT_E4M3                      */
     float eps;          /* > 0                                                   */
@@ -364,8 +364,8 @@ typedef struct cvx_rmsnorm_desc {
  *     h = x + residual                     (h = x without a residual)
  *     q = 1 / sqrt(mean_i(h_i^2) + eps)
  *     sum = h,  y_i = h_i * gamma_i * q    each rounded once to its type
- * h is not rounded before the norm; sums and products are taken in 64 bits, so
- * no finite row overflows them.  With out_dtype = CVX_DT_E4M3,
+ * h enters the norm in 32 bits, whatever its type; sums and products are taken in
+ * 64 bits, so no finite row overflows them.  With out_dtype = CVX_DT_E4M3,
  * u_i = h_i*gamma_i and t = max_i |u_i|,
  *     y_i = e4m3(u_i * (448/t)),  y_scale = t*q/448     (t = 0: zeros)
  * so that y_i * y_scale is the norm's output; q, which depends on the whole
@@ -381,8 +381,8 @@ typedef struct cvx_rmsnorm_desc {
  *   y_scale     : device fp32 [rows]; required iff out_dtype is CVX_DT_E4M3.
  * y, y_scale and sum must not overlap one another or, but for sum as said, an input.
  * Rows aligned to 16 bytes are fastest; others give the same results.
- * Errors: CVX_ERR_NULL, CVX_ERR_SHAPE (rows or c < 1, a stride between 0 and c,
- * more than 2^40 elements from first to last), CVX_ERR_ARG (types, eps),
+ * Errors: CVX_ERR_NULL, CVX_ERR_SHAPE (rows or c < 1, c > 2^30, a stride between 0
+ * and c, more than 2^40 elements from first to last), CVX_ERR_ARG (types, eps),
  * CVX_ERR_ALIGN, CVX_ERR_ALIAS, CVX_ERR_HIP.
  */
 CVX_API cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc *d, const void *x, const void *residual,

@@ -1,7 +1,7 @@
 """cvx_rmsnorm against its definition in 64 bits, element by element.
 
-Tolerances, for a value v of the definition.  The kernel rounds h = x + r, u =
-h*gamma, q and u*q to fp32, at most 2^-24 each, and the output once to its type,
+Tolerances, for a value v of the definition.  The kernel rounds h = x + r and the
+product h*gamma*q to fp32, at most 2^-24 each, and the output once to its type,
 at most eps/2 (or half the smallest subnormal): eps/2 + 5*2^-24 of |v| covers
 them and their products.  `sum` is h rounded twice.  A code is the nearest e4m3 value of u*(448/t): off by half a
 step (2^-4 of the value, 2^-10 below 2^-6) plus four fp32 roundings; its scale
@@ -147,6 +147,15 @@ def test_rmsnorm(case, dt, out8):
 
 
 @pytest.mark.parametrize("out8", [False, True], ids=["same", "e4m3"])
+@pytest.mark.parametrize("dt", [F32, F16, BF16], ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,c", [(257, 1500), (260, 4091), (514, 4004), (515, 8190)])
+def test_rmsnorm_rows_that_fill_the_device(rows, c, dt, out8):
+    # of so many rows each is fewer threads'
+    x, r, g = inputs(rows + c, rows, c, dt)
+    compare(x, r, g, dt, out8, run(x, r, g, dt, out8, (3, 0, 0, 1)), f"{rows}x{c}")
+
+
+@pytest.mark.parametrize("out8", [False, True], ids=["same", "e4m3"])
 @pytest.mark.parametrize("where", ["x", "r"])
 @pytest.mark.parametrize("c", [40, 2051, 40000])
 def test_rmsnorm_sum_in_place(c, where, out8):
@@ -191,6 +200,16 @@ def test_rmsnorm_infinities_and_nans_stay_in_their_rows(c):
         else:
             assert torch.isnan(y[1]).all()
             assert torch.isnan(y[3, c - 1]) and not y[3, :c - 1].any()
+
+
+def test_rmsnorm_an_infinity_that_gamma_hides():
+    x, r, g = inputs(10, 3, 72, BF16)
+    x[1, 7] = float("-inf")
+    g[7] = 0
+    s, y, q = run(x, r, g, BF16, True)
+    assert torch.isnan(q[1]) and torch.isfinite(q[0]) and torch.isfinite(q[2])
+    y = run(x, r, g, BF16, False)[1]
+    assert torch.isnan(y[1, 7]) and not y[1, :7].any() and not y[1, 8:].any()
 
 
 def test_rmsnorm_many_rows():
