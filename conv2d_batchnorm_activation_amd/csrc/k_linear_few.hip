@@ -138,9 +138,10 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
 #pragma unroll
             for (int r = 0; r < RB; ++r) wv[s][r] = *reinterpret_cast<const u32x4*>(p + 2048 * r + l16 * 128 + slot);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)  // eight rows: columns 8 to 15 are of no token
-                xv[s][n] = *reinterpret_cast<const u32x4*>(p + WB + (XR == 8 ? (lane & 7) * 128 + ((4 * s + q) ^ ((lane & 7) >> 1)) * 16
-                                                                                    : (16 * n + l16) * 128 + slot));
+            for (int n = 0; n < NT; ++n) {
+                const int row = XR == 8 ? lane & 7 : 16 * n + l16;  // eight rows: columns 8 to 15 are of no token
+                xv[s][n] = *reinterpret_cast<const u32x4*>(p + WB + row * 128 + ((4 * s + q) ^ (row >> 1 & 7)) * 16);
+            }
             if constexpr (ONE) av[s] = *reinterpret_cast<const u32x4*>(p + AB + l16 * 128 + slot);
         }
         wait_lds();

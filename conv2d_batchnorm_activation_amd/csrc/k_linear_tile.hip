@@ -467,10 +467,21 @@ hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int
 LinPlan linear_plan(const cvx_linear_desc& d)
 {
     LinPlan p;
+    // 4096 -> 4096 channels, bf16: 16 tokens 7.6 us (16.1 by the tile kernel), 32 8.6
+    // (16.5), 64 12.3 (17.9); 64 tokens of rank 16, eight adapters in turn, 21 (40).
+    // Of 8-bit operands 64 tokens to 8192 channels are 16.0 us and would be 11.8 by
+    // tiles, whose instructions drop what this kernel keeps.
     p.few = d.tokens <= 64;
-    p.one = d.tokens == 1 && d.rank > 0 && d.rank <= 16 && d.x_dtype == d.dtype;
+    // The adapter's A is read by every workgroup: 4096 channels to 4096 9.2 us (12.2 with
+    // a launch of its own), to 8192 16.4 (18.4), to 12288 27.1 (27.3), to 14336 35.7
+    // (33.7); 1024 to 16384 17.6 (20.7).
+    p.one = d.tokens == 1 && d.rank > 0 && d.rank <= 16 && d.x_dtype == d.dtype &&
+            (long)d.c_in * d.c_out <= 3l << 24;
     p.nt = d.tokens <= 16 ? 1 : d.tokens <= 32 ? 2 : 4;
-    p.rb = p.nt == 4 && d.c_out >= 32 * 192 ? 2 : 1;
+    // 32 channels a workgroup where 16 would be more than a workgroup a compute unit:
+    // 64 tokens, 4096 channels to 4096 12.6 us (15.5 with 32), to 5120 21.6 (15.9), to
+    // 8192 22.2 (17.3).
+    p.rb = p.nt == 4 && d.c_out > 16 * 256 ? 2 : 1;
     // The tile that ends first by what a stage (128 bytes of every row) and the rest
     // of a tile measured, in 10 ns, with the tiles one a compute unit.  4096 -> 4096
     // channels, bf16: 512 tokens 22 us as 128x64 (256 tiles; 31 as 128x128), 1024
@@ -492,7 +503,12 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     p.slices = p.slice_len = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
     if (d.rank && !p.one) {
-        // slices of c_in until the first product's grid fills the device
+        // Blocks of one token up to 64, of 16 up to 2047, of 64 above.  A whole projection
+        // from 4096 to 4096 channels, tokens by tokens of the same adapter together:
+        // 128 tokens of rank 64 32 us with 16 (38 with one; 154 and 130 if every token has
+        // an adapter of its own), 1024 tokens 53 with 16 (50 with 64), 2048 98 with 16
+        // (88 with 64), 4096 156 (137).  Up to 2047 tokens may be as many requests.
+        // Slices of c_in until the first product's grid fills the device.
         p.down_nb = d.tokens <= 64 ? 0 : d.tokens < 2048 ? 1 : 4;
         p.down_rc = p.down_nb < 4 || d.rank <= 16 ? 1 : d.rank <= 32 ? 2 : 4;
         const int tok = p.down_nb ? 16 * p.down_nb : 1, step = p.down_nb == 4 ? kLoraMany : kLoraChunk;

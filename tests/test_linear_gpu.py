@@ -183,6 +183,15 @@ def test_linear_adapters(shape, dt, x8):
     Case(t * 11 + co, t, ci, co, dt, x8, rank, 1 + t % 13, ids="each").check()
 
 
+@pytest.mark.parametrize("x8", [False, True], ids=["x16", "x8"])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("t,ci,co", [(1, 4096, 12292), (16, 64, 8200), (31, 176, 5000), (33, 80, 4100), (64, 528, 5012)])
+def test_linear_many_channels(t, ci, co, dt, x8):
+    # more than a workgroup a compute unit
+    Case(t + co, t, ci, co, dt, x8, 16, 9, SILU, 2).check()
+    Case(t + ci, t, ci, co, dt, x8).check()
+
+
 @pytest.mark.parametrize("ids", ["runs", "one", "none"])
 @pytest.mark.parametrize("t", [1, 16, 50, 150, 333])
 def test_linear_adapter_ids(t, ids):
@@ -231,6 +240,16 @@ def test_linear_slices_of_wider_tensors(t, x8):
 def test_linear_large_tiles(shape, dt, x8):
     t, ci, co = shape
     c = Case(t, t, ci, co, dt, x8, 16, 5, SILU, 1, ids="runs")
+    c.check()
+    Case(t + 1, t, ci, co, dt, x8, 0, 0).check()
+
+
+@pytest.mark.parametrize("x8", [False, True], ids=["x16", "x8"])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("t,ci,co", [(1000, 80, 4092), (1021, 400, 3972)])
+def test_linear_middle_tiles(t, ci, co, dt, x8):
+    c = Case(t, t, ci, co, dt, x8, 24, 5, SILU, 1)
+    assert "tile 128x128" in c.describe()
     c.check()
     Case(t + 1, t, ci, co, dt, x8, 0, 0).check()
 

@@ -20,6 +20,7 @@ def norm(x=X, r=None, g=G, s=None, y=Y, q=None, **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
+    (dict(rows=1, c=(1 << 30) + 1), SHAPE), (dict(rows=1, c=(1 << 31) - 1), SHAPE),
     (dict(rows=0), SHAPE), (dict(c=0), SHAPE), (dict(rows=-1), SHAPE), (dict(c=-8), SHAPE),
     (dict(x_stride=39), SHAPE), (dict(y_stride=-1), SHAPE), (dict(x_stride=1 << 41), SHAPE),
     (dict(rows=1 << 30, x_stride=1 << 11), SHAPE),           # 2^41 elements from first to last
@@ -100,6 +101,9 @@ def test_linear_queries():
     # one token takes up to 16 ranks in the projection's own kernel
     assert cvx.cvx_linear_workspace_bytes(lin_desc(tokens=1, rank=16, n_adapters=3)) == 0
     assert cvx.cvx_linear_workspace_bytes(lin_desc(tokens=1, rank=24, n_adapters=3)) > 0
+    # ... of weights up to 3 * 2^24 values
+    assert cvx.cvx_linear_workspace_bytes(lin_desc(tokens=1, c_in=4096, c_out=12288, rank=16, n_adapters=3)) == 0
+    assert cvx.cvx_linear_workspace_bytes(lin_desc(tokens=1, c_in=4096, c_out=12292, rank=16, n_adapters=3)) > 0
     for t in (2, 17, 64, 65, 300, 5000):
         d = lin_desc(tokens=t, c_in=4096, rank=16, n_adapters=3)
         need = cvx.cvx_linear_workspace_bytes(d)
