@@ -321,15 +321,22 @@ def make_rmsnorm_desc(rows, c, dtype, out_dtype=None, eps=1e-6, x_stride=0, res_
                             sum_stride, y_stride)
 
 
+def _gpu_ptr(t) -> Optional[int]:
+    """_ptr of what an operator on tokens is given; host tensors are refused."""
+    if t is None or t.__class__ is int:
+        return t
+    if not t.is_cuda:
+        raise ValueError("tensors have to be on a GPU")
+    return t.data_ptr()
+
+
 def _elsewhere(x, call, *args) -> bool:
     """Operators on tokens run on their input's device: where that is not the current
-    one, makes it current, calls again and says so.  Host tensors are refused."""
+    one, makes it current, calls again and says so."""
     if not isinstance(x, torch.Tensor):
         return False
     dev = x.get_device()
-    if dev < 0:
-        raise ValueError("tensors have to be on a GPU")
-    if dev == torch.cuda.current_device():
+    if dev < 0 or dev == torch.cuda.current_device():
         return False
     with torch.cuda.device(dev):
         call(*args)
@@ -339,8 +346,8 @@ def _elsewhere(x, call, *args) -> bool:
 def cvx_rmsnorm(desc: cvx_rmsnorm_desc, x, residual, gamma, sum_out, y, y_scale=None, stream=None) -> None:
     if _elsewhere(x, cvx_rmsnorm, desc, x, residual, gamma, sum_out, y, y_scale, stream):
         return
-    _check(lib.cvx_rmsnorm(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum_out), _ptr(y),
-                           _ptr(y_scale), _stream(stream)), "cvx_rmsnorm")
+    _check(lib.cvx_rmsnorm(ctypes.byref(desc), _gpu_ptr(x), _gpu_ptr(residual), _gpu_ptr(gamma), _gpu_ptr(sum_out),
+                           _gpu_ptr(y), _gpu_ptr(y_scale), _stream(stream)), "cvx_rmsnorm")
 
 
 def make_linear_desc(tokens, c_in, c_out, dtype, x_dtype=None, act=CVX_ACT_NONE, res_mode=CVX_RES_NONE, rank=0,
@@ -368,6 +375,7 @@ def cvx_linear(desc: cvx_linear_desc, x, w, y, x_scale=None, scale=None, bias=No
     if _elsewhere(x, cvx_linear, desc, x, w, y, x_scale, scale, bias, residual, lora_a, lora_b, lora_alpha, lora_id,
                   workspace, ws_bytes, stream):
         return
-    _check(lib.cvx_linear(ctypes.byref(desc), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(scale), _ptr(bias),
-                          _ptr(residual), _ptr(lora_a), _ptr(lora_b), _ptr(lora_alpha), _ptr(lora_id), _ptr(y),
-                          _ptr(workspace), ws_bytes, _stream(stream)), "cvx_linear")
+    _check(lib.cvx_linear(ctypes.byref(desc), _gpu_ptr(x), _gpu_ptr(x_scale), _gpu_ptr(w), _gpu_ptr(scale),
+                          _gpu_ptr(bias), _gpu_ptr(residual), _gpu_ptr(lora_a), _gpu_ptr(lora_b),
+                          _gpu_ptr(lora_alpha), _gpu_ptr(lora_id), _gpu_ptr(y), _gpu_ptr(workspace), ws_bytes,
+                          _stream(stream)), "cvx_linear")

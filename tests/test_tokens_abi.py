@@ -130,3 +130,14 @@ def test_host_tensors_are_refused():
         cvx.cvx_rmsnorm(cvx.make_rmsnorm_desc(8, 64, F32), t, None, t[0], None, t.clone())
     with pytest.raises(ValueError):
         cvx.cvx_linear(lin_desc(tokens=8, c_out=64), t, t, t.clone())
+    # ... whichever they are: the rest are addresses here, which no call is made with
+    for i in range(1, 6):
+        args = [X, R, SC, W, Y, Q]
+        args[i] = t
+        with pytest.raises(ValueError):
+            cvx.cvx_rmsnorm(cvx.make_rmsnorm_desc(8, 64, F32, E4M3), *args)
+    for i in range(1, 12):
+        args = [X, W, Y, Q, SC, BI, R, LA, LB, AL, ID, WS]
+        args[i] = t
+        with pytest.raises(ValueError):
+            cvx.cvx_linear(lin_desc(tokens=8, c_out=64), *args)
