@@ -3,13 +3,19 @@
 //
 // The weights are the A operand (rows = output channels) and the tokens the B
 // operand (columns = tokens), so a lane's accumulators are channels of one
-// token.  A stage is 128 bytes of
-// every row of both operands, loaded straight into LDS; the 16-byte pieces of a
-// row are permuted by the row's index as they are fetched, so that the lanes of
-// an operand read (32 rows, the same piece) fall in different banks while every
-// fetch still takes whole 128-byte lines.  Two stage buffers: stage s+1 arrives
-// while s is multiplied, with one barrier a stage, which comes before the
-// stage's last step so that the next stage's first operands are read under it.
+// token.  A stage is 128 bytes of every row of both operands, loaded straight
+// into LDS; the 16-byte pieces of a row are permuted by the row's index as they
+// are fetched, so that the lanes of an operand read (32 rows, the same piece) fall
+// in different banks while every fetch still takes whole 128-byte lines.  Stage
+// s+1 (and, with four stage buffers, up to s+3) arrives while s is multiplied; a
+// stage has one barrier, before which a wave waits for its own fetches of the next
+// stage only, and which drains nothing: a fence there waited for every fetch under
+// way (512 tokens, 4096 -> 4096 channels, 34 us instead of 22).
+//
+// The matrix cores bound the large ones: 4096^3 bf16 105 to 114 us (1200 to 1310
+// TFLOP/s), 8192 x 4096 x 14336 e4m3 386 us (2490).  512 tokens, 4096 -> 4096: 22
+// us, 256 workgroups of one tile, bound by the cache's rate (24 KB a stage of 0.28
+// us in every compute unit).
 //
 // 8-bit operands (e4m3) are the same bytes: a stage is 128 channels instead of
 // 64, and the 32x32x64 instruction takes two pieces a lane where the 16-bit
@@ -35,7 +41,6 @@
 namespace cvx {
 
 namespace {
-
 
 // Orders this wave's LDS accesses (which the hardware keeps in order) for the compiler.
 __device__ __forceinline__ void wave_lds_order()

@@ -5,15 +5,21 @@
 // A wave holds 16 tokens' values of 256 channels in registers as the matrix
 // instruction's B operand, and goes through the distinct adapters of its tokens:
 // each adapter's 16 x 256 block of A streams past once, and the lanes (one token
-// each) whose token names that adapter keep the product.  So a block of tokens
-// of one request costs one pass, tokens of many requests cost their adapters'
-// bytes, and a value of another adapter never enters a token's sum.  Where there
-// are few tokens, each likely of a request of its own, a block is one token:
-// the passes over adapters are then workgroups side by side.  The four waves of a workgroup take the four quarters
-// of 1024 channels and add their sums in LDS in a fixed order; a workgroup
-// covers a slice of whole such steps, and the slices of c_in that make up the
-// grid when there are few tokens are added, in order, by the kernel that reads
-// them.
+// each) whose token names that adapter keep the product.  So a block of tokens of
+// one request costs one pass, tokens of many requests cost their adapters' bytes,
+// and a value of another adapter never enters a token's sum.  Where there are few
+// tokens, each likely of a request of its own, a block is one token: the passes
+// over adapters are then workgroups side by side.  The four waves of a workgroup
+// take the four quarters of 1024 channels and add their sums in LDS in a fixed
+// order; a workgroup covers a slice of whole such steps, and the slices of c_in
+// that make up the grid when there are few tokens are added, in order, by the
+// kernel that reads them.
+//
+// Latency bounds the small ones, the address unit the larger.  Measured, 4096
+// channels bf16: 48 tokens of as many adapters, rank 32, 5.5 us; 512 tokens, rank
+// 16, 5.7; 4096 tokens in 64s (k_lora_down_many), rank 16, 10.5 (14.5 in registers,
+// with consecutive blocks on all XCDs); 8192 tokens of e4m3, rank 64, 29.  Joining
+// the slices: 2.5 to 5 us.
 #include "lin_common.h"
 
 #include "cvx_internal.h"
