@@ -189,8 +189,12 @@ cvx_status cvx_linear(const cvx_linear_desc* d, const void* x, const float* x_sc
             if (i.p && meets(wsp, i.s)) return CVX_ERR_ALIAS;
     }
     a.part = static_cast<float*>(workspace);
-    a.joined = static_cast<char*>(workspace) + (size_t)p.slices * d->tokens * d->rank * sizeof(float);
-    a.down = reinterpret_cast<float*>(static_cast<char*>(a.joined) + lora_joined_bytes(d->tokens, d->rank));
+    a.joined = nullptr;
+    a.down = nullptr;
+    if (p.join) {
+        a.joined = static_cast<char*>(workspace) + (size_t)p.slices * d->tokens * d->rank * sizeof(float);
+        a.down = reinterpret_cast<float*>(static_cast<char*>(a.joined) + lora_joined_bytes(d->tokens, d->rank));
+    }
     a.tokens = d->tokens;
     a.cin = d->c_in;
     a.cout = d->c_out;
@@ -203,7 +207,7 @@ cvx_status cvx_linear(const cvx_linear_desc* d, const void* x, const float* x_sc
     a.tiles_m = a.tiles_n = 0;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (lora && !p.one && launch_lora_down(a, p, d->dtype, x8, s) != hipSuccess) return CVX_ERR_HIP;
-    if (lora && !p.few && launch_lora_join(a, d->dtype, s) != hipSuccess) return CVX_ERR_HIP;
+    if (p.join && launch_lora_join(a, d->dtype, s) != hipSuccess) return CVX_ERR_HIP;
     const hipError_t e = p.few ? launch_linear_few(a, p, d->dtype, x8, s) : launch_linear_tile(a, p, d->dtype, x8, s);
     return e == hipSuccess ? CVX_OK : CVX_ERR_HIP;
 }

@@ -29,7 +29,7 @@
 // second product of the adapters is accumulated onto them by the same matrix
 // instructions: for every 32 tokens, each distinct adapter's rows of B, with v
 // as two 16-bit values (v = high + low, so v keeps 16 bits in bf16 and 21 in
-// fp16; k_lora_join makes them); the lanes whose token names the adapter keep the
+// fp16; k_lora_join makes them, or the tile itself); the lanes whose token names the adapter keep the
 // result.  fp16, whose range v may leave, takes v and the sums divided by a power
 // of two per token.
 #include <stdio.h>
@@ -318,13 +318,30 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
             // this lane's pieces of v: [eight ranks][part][token]; past the last token, its
             const long here = n0 + t < a.tokens ? n0 + t : a.tokens - 1;
             const u32x4* v = reinterpret_cast<const u32x4*>(a.joined) + (2l * hi * a.tokens + here);
-            float down = 1.0f, up = 1.0f;
-            if constexpr (!V16<T>::BF) {
-                if (id >= 0) {
-                    down = a.down[here];
-                    up = 1.0f / down;  // a power of two: exact
+            float down = 1.0f;
+            u32x4 vh0, vl0;  // the first sixteen ranks' pieces
+            if constexpr (D == 4) {
+                if (a.joined) {
+                    vh0 = v[0];
+                    vl0 = v[a.tokens];
+                    if (!V16<T>::BF && id >= 0) down = a.down[here];
+                } else {  // up to sixteen ranks, joined here
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+                    if (id >= 0 && 8 * hi < a.rank) lora_values(a, id, here, 8 * hi, f);
+                    if constexpr (!V16<T>::BF) {
+                        const float top = lora_top(f);
+                        down = lora_factor(fmaxf(top, __shfl_xor(top, 32)));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] *= down;
+                    }
+                    lora_parts<T>(f, vh0, vl0);
                 }
+            } else if (!V16<T>::BF && id >= 0) {
+                down = a.down[here];
             }
+            const float up = 1.0f / down;  // a power of two: exact
             while (todo) {  // each pass clears at least the first bit
                 const int d = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
                 const bool mine = id == d;
@@ -354,7 +371,11 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
                             if (r0 + 16 * s < a.rank) {
-                                const u32x4 vh = v[(r0 / 4 + 4l * s) * a.tokens], vl = v[(r0 / 4 + 4l * s + 1) * a.tokens];
+                                u32x4 vh = vh0, vl = vl0;
+                                if (D != 4 || r0 + s > 0) {
+                                    vh = v[(r0 / 4 + 4l * s) * a.tokens];
+                                    vl = v[(r0 / 4 + 4l * s + 1) * a.tokens];
+                                }
 #pragma unroll
                                 for (int m = 0; m < 2; ++m) c[m] = mma32<T>(b[s][m], vl, c[m]);
 #pragma unroll
@@ -505,7 +526,7 @@ LinPlan linear_plan(const cvx_linear_desc& d)
         p.mb = t.mb;
         p.nb = t.nb;
     }
-    p.slices = p.slice_len = p.down_nb = p.down_rc = 0;
+    p.slices = p.slice_len = p.join = p.down_nb = p.down_rc = 0;
     p.ws_bytes = 0;
     if (d.rank && !p.one) {
         // Blocks of one token up to 64, of 16 up to 2047, of 64 above.  A whole projection
@@ -525,7 +546,11 @@ LinPlan linear_plan(const cvx_linear_desc& d)
         p.slice_len = per * step;
         p.slices = (int)((chunks + per - 1) / per);
         p.ws_bytes = (size_t)p.slices * d.tokens * d.rank * sizeof(float);
-        if (!p.few) p.ws_bytes += lora_joined_bytes(d.tokens, d.rank) + (size_t)d.tokens * sizeof(float);
+        // Tiles of one wave a SIMD have registers for the slices of up to 16 ranks: there
+        // each joins its tokens' itself, which spares a launch (512 tokens 4096 -> 4096
+        // channels, rank 16: 32.7 -> 30.4 us).  More ranks are as many loads at every tile's end.
+        p.join = !p.few && (p.mb == 4 || d.rank > 16 || p.slices > 8);
+        if (p.join) p.ws_bytes += lora_joined_bytes(d.tokens, d.rank) + (size_t)d.tokens * sizeof(float);
     }
     return p;
 }

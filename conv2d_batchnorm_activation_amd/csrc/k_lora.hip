@@ -222,14 +222,11 @@ __global__ void __launch_bounds__(256) k_lora_down_many(LinArgs a)
     }
 }
 
-// The slices of v added, in order, times the adapter's factor, and taken apart into
-// two 16-bit values, once for all the tiles of output channels that read them.  A
-// token's ranks are eight a lane; fp16 scales them by 2^-e, e the exponent of the
-// token's largest |v|.  Tokens without an adapter get zeros, which nothing reads.
+// v joined and taken apart into two 16-bit values, once for all the tiles of output
+// channels that read them; a token's ranks are eight a lane.  Tokens without an adapter get zeros, which nothing reads.
 template <typename T>
 __global__ void __launch_bounds__(256) k_lora_join(LinArgs a)
 {
-    typedef typename V16<T>::v8 v8;
     int lanes = 2;  // that share a token: a power of two, of whole sixteens of ranks
     while (8 * lanes < a.rank) lanes *= 2;
     const long at = (long)blockIdx.x * 256 + threadIdx.x;
@@ -239,53 +236,18 @@ __global__ void __launch_bounds__(256) k_lora_join(LinArgs a)
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-    if (id >= 0 && r < a.rank) {
-        const float* p = a.part + token * a.rank + r;
-        for (int s = 0; s < a.slices; s += 4) {
-            f32x4 p0[4], p1[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float* q = p + (long)(s + k) * a.tokens * a.rank;
-                p0[k] = p1[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                if (s + k < a.slices) {
-                    p0[k] = *reinterpret_cast<const f32x4*>(q);
-                    p1[k] = *reinterpret_cast<const f32x4*>(q + 4);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] += p0[k][e];
-                    v[4 + e] += p1[k][e];
-                }
-        }
-        const float alpha = a.lora_alpha ? a.lora_alpha[id] : 1.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= alpha;
-    }
+    if (id >= 0 && r < a.rank) lora_values(a, id, token, r, v);
     if constexpr (!V16<T>::BF) {
-        float top = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+        float top = lora_top(v);
         for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
-        int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
-        e = e < -24 ? -24 : e > 120 ? 120 : e;
-        const float down = __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
+        const float down = lora_factor(top);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= down;
         if (r == 0 && token < a.tokens) a.down[token] = down;
     }
     if (token < a.tokens && r < (a.rank + 15) / 16 * 16) {
-        v8 high, low;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            high[e] = (T)v[e];
-            low[e] = __builtin_isfinite((float)high[e]) ? (T)(v[e] - (float)high[e]) : (T)0.0f;
-        }
         u32x4* out = static_cast<u32x4*>(a.joined) + 2l * r8 * a.tokens + token;
-        out[0] = __builtin_bit_cast(u32x4, high);
-        out[a.tokens] = __builtin_bit_cast(u32x4, low);
+        lora_parts<T>(v, out[0], out[a.tokens]);
     }
 }
 

@@ -101,6 +101,68 @@ __device__ __forceinline__ int adapter_of(const LinArgs& a, int token)
     return d >= 0 && d < a.n_adapters ? d : -1;
 }
 
+// Ranks r to r+7 of v of a token with adapter d: its slices added, in order, times
+// the adapter's factor.
+__device__ __forceinline__ void lora_values(const LinArgs& a, int d, long token, int r, float (&v)[8])
+{
+    const float* p = a.part + token * a.rank + r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    for (int s = 0; s < a.slices; s += 4) {
+        f32x4 p0[4], p1[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float* q = p + (long)(s + k) * a.tokens * a.rank;
+            p0[k] = p1[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (s + k < a.slices) {
+                p0[k] = *reinterpret_cast<const f32x4*>(q);
+                p1[k] = *reinterpret_cast<const f32x4*>(q + 4);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += p0[k][e];
+                v[4 + e] += p1[k][e];
+            }
+    }
+    const float alpha = a.lora_alpha ? a.lora_alpha[d] : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= alpha;
+}
+
+// The largest |v| of eight.
+__device__ __forceinline__ float lora_top(const float (&v)[8])
+{
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+    return top;
+}
+
+// fp16: the power of two a token's v is multiplied by, 2^-e, e the exponent of its largest |v|.
+__device__ __forceinline__ float lora_factor(float top)
+{
+    int e = (int)((__builtin_bit_cast(unsigned, top) >> 23) & 255u) - 127;
+    e = e < -24 ? -24 : e > 120 ? 120 : e;
+    return __builtin_bit_cast(float, (unsigned)(127 - e) << 23);
+}
+
+// v as the sum of two 16-bit values.
+template <typename T>
+__device__ __forceinline__ void lora_parts(const float (&v)[8], u32x4& high, u32x4& low)
+{
+    typename V16<T>::v8 h, l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        h[e] = (T)v[e];
+        l[e] = __builtin_isfinite((float)h[e]) ? (T)(v[e] - (float)h[e]) : (T)0.0f;
+    }
+    high = __builtin_bit_cast(u32x4, h);
+    low = __builtin_bit_cast(u32x4, l);
+}
+
 // z (scale, bias, adapters in it) -> y
 __device__ __forceinline__ float finish(float z, float r, int act, int res_mode)
 {

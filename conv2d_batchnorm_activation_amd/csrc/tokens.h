@@ -41,7 +41,8 @@ struct LinArgs {
     void* y;
     float* part;           // low-rank values [slices][tokens][rank], fp32
     void* joined;          // tile kernel: the same, joined, as high and low 16-bit parts:
-                           // [rank/8, to a multiple of two][part][token] pieces of eight
+                           // [rank/8, to a multiple of two][part][token] pieces of eight; or
+                           // null, where the tiles join them
     float* down;           // tile kernel, fp16: per token, the power of two they are multiplied by
     long xs, rs, ys;       // row strides, elements
     int tokens, cin, cout;
@@ -59,6 +60,7 @@ struct LinPlan {
     int nt, rb;          // few: 16-token blocks and 16-channel blocks a workgroup holds
     int mb, nb;          // tile: 64*mb channels x 64*nb tokens
     int slices, slice_len;
+    int join;              // tile: the first product's slices are joined by a kernel of their own
     int down_nb, down_rc;  // first product: 16-token blocks (0: one token) and 16-rank blocks a workgroup
     size_t ws_bytes;
 };

@@ -215,6 +215,13 @@ def test_linear_adapters_of_prompts(rank, dt, x8):
     Case(rank, 2070, 1168, 68, dt, x8, rank, 7, ids="runs").check()
 
 
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("ci,rank", [(1040, 8), (8192, 16), (8208, 16), (2064, 24)])
+def test_linear_adapters_in_slices(ci, rank, dt):
+    # the first product in few slices, joined by the tiles, and in many or of more ranks, joined before
+    Case(ci, 100, ci, 68, dt, False, rank, 40).check()
+
+
 @pytest.mark.parametrize("t", [3, 40, 140])
 @pytest.mark.parametrize("act", [NONE, RELU, SILU])
 @pytest.mark.parametrize("res", [0, 1, 2])
@@ -251,6 +258,7 @@ def test_linear_middle_tiles(t, ci, co, dt, x8):
     c = Case(t, t, ci, co, dt, x8, 24, 5, SILU, 1)
     assert "tile 128x128" in c.describe()
     c.check()
+    Case(t + 2, t, ci, co, dt, x8, 8, 7, ids="runs").check()
     Case(t + 1, t, ci, co, dt, x8, 0, 0).check()
 
 
