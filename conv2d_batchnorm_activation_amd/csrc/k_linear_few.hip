@@ -79,7 +79,6 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     static_assert(BESIDE > 0 && 4 * MOST <= W * SB && 4 * 256 * RB * NT <= W * SB, "they fit a stage");
     __shared__ __attribute__((aligned(16))) float vbeside[BESIDE];
     __shared__ int id_lds[16 * NT];
-    __shared__ float alpha_lds[16 * NT];
     const bool beside = a.tokens * a.rank <= BESIDE;
     float* vlds = ONE || beside ? vbeside : reinterpret_cast<float*>(st1);
     const int tid = threadIdx.x, lane = tid & 63;
@@ -178,13 +177,16 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] += p[k][e];
             }
-            const float al = alpha_lds[i / a.rank];
+            const int d = id_lds[i / a.rank];
+            const float al = d >= 0 && a.lora_alpha ? a.lora_alpha[d] : 1.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] *= al;
             *reinterpret_cast<f32x4*>(vlds + i) = v;
         }
     };
-    // stages past the last are zeros
+    // Loads return in their order: what the loads of the end need goes first, those loads
+    // behind the first stages' fetches.  Stages past the last are zeros.
+    const int id = a.rank && tid < 16 * NT ? adapter_of(a, tid) : -1;
     issue(0, st0);
     issue(1, st1);
     issue(2, st2);
@@ -194,22 +196,19 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     constexpr int CH = 16 * RB, TSTEP = 64 * W / CH, ITEMS = (16 * NT + TSTEP - 1) / TSTEP;
     const int ch = tid % CH, tfirst = tid / CH, c = c0 + ch;
     const float sc = a.scale && c < a.cout ? a.scale[c] : 1.0f, bi = a.bias && c < a.cout ? a.bias[c] : 0.0f;
-    float sx[ITEMS], res[ITEMS];
+    float sx[ITEMS];
+    T res[ITEMS];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int t = tfirst + TSTEP * k;
         const bool ok = t < a.tokens && c < a.cout;
         sx[k] = X8 && ok ? a.x_scale[t] : 1.0f;
-        res[k] = a.res && ok ? (float)static_cast<const T*>(a.res)[(long)t * a.rs + c] : 0.0f;
+        res[k] = a.res && ok ? static_cast<const T*>(a.res)[(long)t * a.rs + c] : (T)0.0f;
     }
     if (a.rank) {
-        if (tid < 16 * NT) {
-            const int d = adapter_of(a, tid);
-            id_lds[tid] = d;
-            alpha_lds[tid] = d >= 0 && a.lora_alpha ? a.lora_alpha[d] : 1.0f;
-        }
-        lds_barrier();
-        if (!ONE && beside) low_rank();
+        if (tid < 16 * NT) id_lds[tid] = id;
+        wait_lds();
+        stage_barrier();  // (which waits for no fetch)
     }
     // The low-rank term.  Lanes take the adapters' rows as they lie in memory, eight
     // ranks each, the first EARLY of a lane's pieces now; the `lanes` of a channel
@@ -248,6 +247,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     v8 early[EARLY];
 #pragma unroll
     for (int k = 0; k < EARLY; ++k) early[k] = load_b(tid + NTH * k);
+    if (!ONE && a.rank && beside) low_rank();
     for (int i = 0; i < steps; i += D) {
         stage(i, st0);
         stage(i + 1, st1);
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < W; ++w) v += lows[16 * w + tid];
-            vlds[tid] = v * alpha_lds[0];
+            vlds[tid] = v * (one >= 0 && a.lora_alpha ? a.lora_alpha[one] : 1.0f);
         }
     }
     __syncthreads();
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
             z += redf[(((w * RB + (ch >> 4)) * NT + (t >> 4)) * 64 + ((ch & 15) >> 2) * 16 + (t & 15)) * 4 + (ch & 3)];
         z = fmaf(X8 ? z * sx[k] : z, sc, bi);
         if (a.rank) z += us[t * CH + ch];
-        static_cast<T*>(a.y)[(long)t * a.ys + c] = (T)finish(z, res[k], a.act, a.res_mode);
+        static_cast<T*>(a.y)[(long)t * a.ys + c] = (T)finish(z, (float)res[k], a.act, a.res_mode);
     }
 }
 
