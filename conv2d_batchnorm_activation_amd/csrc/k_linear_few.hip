@@ -1,7 +1,8 @@
-// k_linear_few.hip -- projection of few tokens (up to 64), the form for
-// generated tokens: bound by the stream of the weights.
+// k_linear_few.hip -- projection of few tokens, the form for generated tokens:
+// bound by the stream of the weights.
 //
-// A workgroup takes 16*RB output channels and all tokens; its W waves take
+// A workgroup takes 16*RB output channels and all tokens (of more than 64, a block
+// of 64); its W waves take
 // 128-byte pieces of the weight rows in turn.  A wave loads its pieces straight
 // into LDS of its own, four lines of 1 KB ahead and more (D stages, no barrier:
 // a wave waits for its own loads only), with whole 128-byte lines a fetch: loaded
@@ -79,6 +80,18 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     static_assert(BESIDE > 0 && 4 * MOST <= W * SB && 4 * 256 * RB * NT <= W * SB, "they fit a stage");
     __shared__ __attribute__((aligned(16))) float vbeside[BESIDE];
     __shared__ int id_lds[16 * NT];
+    // a block of tokens: its rows of every operand
+    const long slice = (long)a.tokens * a.rank;  // of v's partial sums
+    const int t0 = blockIdx.y * 16 * NT;
+    a.tokens = a.tokens - t0 < 16 * NT ? a.tokens - t0 : 16 * NT;
+    a.x = static_cast<const char*>(a.x) + t0 * a.xs * XB;
+    a.y = static_cast<T*>(a.y) + t0 * a.ys;
+    if (X8) a.x_scale += t0;
+    if (a.res) a.res = static_cast<const T*>(a.res) + t0 * a.rs;
+    if (a.rank) {
+        a.lora_id += t0;
+        a.part += (long)t0 * a.rank;
+    }
     const bool beside = a.tokens * a.rank <= BESIDE;
     float* vlds = ONE || beside ? vbeside : reinterpret_cast<float*>(st1);
     const int tid = threadIdx.x, lane = tid & 63;
@@ -170,7 +183,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
                 f32x4 p[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    p[k] = s + k < a.slices ? *reinterpret_cast<const f32x4*>(a.part + (long)(s + k) * total + i)
+                    p[k] = s + k < a.slices ? *reinterpret_cast<const f32x4*>(a.part + (s + k) * slice + i)
                                             : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -306,8 +319,8 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
 template <typename T, bool X8, int W, int RB, int NT, int XR, int D, bool ONE = false>
 void launch_few_k(const LinArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_linear_few<T, X8, ONE, W, RB, NT, XR, D>), dim3((unsigned)((a.cout + 16 * RB - 1) / (16 * RB))),
-                       dim3(64 * W), 0, s, a);
+    const dim3 grid((unsigned)((a.cout + 16 * RB - 1) / (16 * RB)), (unsigned)((a.tokens + 16 * NT - 1) / (16 * NT)));
+    hipLaunchKernelGGL((k_linear_few<T, X8, ONE, W, RB, NT, XR, D>), grid, dim3(64 * W), 0, s, a);
 }
 
 template <typename T, bool X8>
@@ -336,7 +349,6 @@ hipError_t launch_few_t(const LinArgs& a, const LinPlan& p, hipStream_t s)
 
 hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s)
 {
-    if (a.tokens > 16 * p.nt) return hipErrorInvalidValue;
     if (dtype == CVX_DT_F16) return x8 ? launch_few_t<half_t, true>(a, p, s) : launch_few_t<half_t, false>(a, p, s);
     return x8 ? launch_few_t<bf16_t, true>(a, p, s) : launch_few_t<bf16_t, false>(a, p, s);
 }

@@ -497,7 +497,15 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     // (16.5), 64 12.3 (17.9); 64 tokens of rank 16, eight adapters in turn, 21 (40).
     // Of 8-bit operands 64 tokens to 8192 channels are 16.0 us and would be 11.8 by
     // tiles, whose instructions drop what this kernel keeps.
-    p.few = d.tokens <= 64;
+    // More tokens go there in blocks of 64 where that is at most a workgroup a compute
+    // unit, as there would be fewer tiles still, and c_in is long enough: 128 tokens to
+    // 2048 channels from 4096 12.8 us (18.1 by tiles), from 2048 8.3 (11.2), of rank 16
+    // 17.0 (18.6); 256 tokens, 4096 to 1024, rank 32 23.4 (27.8), rank 64 30.7 (29.5);
+    // 200 tokens, 8192 to 1024, rank 64 39 (47); 1024 tokens, 1024 to 256, rank 16 16.6
+    // (13.6).
+    p.few = d.tokens <= 64 ||
+            (d.x_dtype == d.dtype && d.c_in >= 64 * (d.rank > 32 ? d.rank : 32) &&
+             (long)((d.c_out + 15) / 16) * ((d.tokens + 63) / 64) <= 256);
     // The adapter's A is read by every workgroup: 4096 channels to 4096 9.2 us (12.2 with
     // a launch of its own), to 8192 16.4 (18.4), to 12288 27.1 (27.3), to 14336 35.7
     // (33.7); 1024 to 16384 17.6 (20.7).

@@ -57,7 +57,8 @@ struct LinArgs {
 struct LinPlan {
     int few;             // 1: the kernel for few tokens; 0: the tile kernel
     int one;             // few: a single token, the adapter's first product in the same kernel
-    int nt, rb;          // few: 16-token blocks and 16-channel blocks a workgroup holds
+    int nt, rb;          // few: 16-token blocks and 16-channel blocks a workgroup holds; a grid
+                         // row is 16*nt tokens
     int mb, nb;          // tile: 64*mb channels x 64*nb tokens
     int slices, slice_len;
     int join;              // tile: the first product's slices are joined by a kernel of their own

@@ -162,7 +162,7 @@ SHAPES = [
     # tokens, c_in, c_out
     (1, 16, 4), (1, 512, 64), (2, 48, 20), (15, 1040, 36), (16, 2064, 16), (17, 80, 300), (31, 4112, 24), (33, 160, 132),
     (64, 1024, 260), (65, 16, 4), (65, 64, 128), (97, 208, 36), (128, 144, 132), (129, 1040, 260), (200, 64, 516),
-    (257, 336, 100), (300, 2064, 384),
+    (257, 336, 100), (300, 2064, 384), (129, 2064, 1364),
 ]
 
 
@@ -216,10 +216,22 @@ def test_linear_adapters_of_prompts(rank, dt, x8):
 
 
 @pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("co", [68, 2052])
 @pytest.mark.parametrize("ci,rank", [(1040, 8), (8192, 16), (8208, 16), (2064, 24)])
-def test_linear_adapters_in_slices(ci, rank, dt):
+def test_linear_adapters_in_slices(ci, rank, co, dt):
     # the first product in few slices, joined by the tiles, and in many or of more ranks, joined before
-    Case(ci, 100, ci, 68, dt, False, rank, 40).check()
+    Case(ci, 100, ci, co, dt, False, rank, 40).check()
+
+
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("t,ci,co,rank", [(65, 2048, 2048, 0), (129, 2056, 1348, 16), (190, 4104, 132, 64),
+                                          (500, 2064, 508, 32), (2100, 2200, 20, 8), (70, 8200, 36, 128)])
+def test_linear_blocks_of_few_tokens(t, ci, co, rank, dt):
+    # few tiles of a long row: the kernel for few tokens takes them 64 at a time
+    c = Case(t, t, ci, co, dt, False, rank, 9 if rank else 0, SILU, 2, pads=(24, 8, 12))
+    assert "linear few 16x64" in c.describe()
+    c.check()
+    Case(t + 1, t, ci, co, dt, False, rank, 3 if rank else 0, ids="runs").check()
 
 
 @pytest.mark.parametrize("t", [3, 40, 140])
