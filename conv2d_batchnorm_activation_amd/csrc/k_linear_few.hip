@@ -16,8 +16,8 @@
 // from LDS, the adapters' rows of these channels from memory.
 //
 // Measured, the rate that of the weights: one token, 4096 -> 4096 channels bf16 7.5
-// us (4.5 TB/s), with an adapter of rank 16 9.0; 16 tokens of e4m3, 8192 -> 8192
-// 15.0 (4.5), with 16 adapters of rank 16 21.4; 48 tokens bf16, 4096 -> 8192 16.6
+// us (4.5 TB/s), with an adapter of rank 16 8.7; 16 tokens of e4m3, 8192 -> 8192
+// 15.0 (4.5), with 16 adapters of rank 16 21.3; 48 tokens bf16, 4096 -> 8192 16.6
 // (4.0), with 32 adapters of rank 32 34.  A copy of such weights runs at 5.4 TB/s;
 // what is missing is a workgroup's first fetch and its end, as each compute unit
 // has one or two workgroups in all.

@@ -22,7 +22,7 @@
 //
 // Measured: 16384 rows of 4096 bf16 channels with residual and sum to e4m3 86 us,
 // 5.4 TB/s, the rate of a copy of that size; 96 rows of 8192 fp16 channels 4.2 us
-// and one row of 4096 2.9 us, latency; 2048 rows of 20480 fp32 channels 135 us, 5.0
+// and one row of 4096 2.7 us, latency; 2048 rows of 20480 fp32 channels 135 us, 5.0
 // TB/s, 512 rows 39 us, 4.3 TB/s.  A row of 20480 by 512 threads instead of 1024:
 // 300 rows 20.7 us (23.9), 2048 rows 143 (135).
 #include "cvx_internal.h"
