@@ -1,8 +1,8 @@
 // api_tokens.hip -- the C ABI of the operators on tokens: host-side validation
 // and the choice of kernels.  Every check runs on the host before anything is
 // enqueued.
+#include <float.h>
 #include <stdint.h>
-#include <stdio.h>
 
 #include "cvx_internal.h"
 #include "tokens.h"
@@ -79,7 +79,7 @@ cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc* d, const void* x, const void* res
     if (d == nullptr) return CVX_ERR_NULL;
     if (d->dtype != CVX_DT_F32 && !dtype16(d->dtype)) return CVX_ERR_ARG;
     if (d->out_dtype != d->dtype && d->out_dtype != CVX_DT_E4M3) return CVX_ERR_ARG;
-    if (!(d->eps > 0.0f)) return CVX_ERR_ARG;
+    if (!(d->eps > 0.0f) || d->eps > FLT_MAX) return CVX_ERR_ARG;
     if (d->rows < 1 || d->c < 1 || d->c > kMaxNormed) return CVX_ERR_SHAPE;
     const bool out8 = d->out_dtype == CVX_DT_E4M3;
     RmsArgs a;

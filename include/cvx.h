@@ -4,13 +4,14 @@
  *
  * Conventions shared by every call
  * --------------------------------
- *  - Tensors are fp32, dense and contiguous.  Activations are NCHW: element
+ *  - Tensors are fp32, dense and contiguous, unless their call says otherwise (the
+ *    channels-last layer, the operators on tokens).  Activations are NCHW: element
  *    (n, c, h, w) sits at n*C*H*W + c*H*W + h*W + w ("YOLO26N Inference
  *    Optimisation", section "NHWC migration", "What NHWC is and why it matters").
  *    Convolution weights are OIHW: [c_out][c_in/groups][kh][kw], the order the
  *    MNIST page's PyTorch weights use ("Как я свертки ускорял", "Ускоряем скорость").
  *  - Every tensor pointer is a DEVICE pointer (HBM), 4-byte aligned, unless the
- *    argument says "host".  The caller owns all memory; the library borrows the
+ *    argument says "host" or another alignment.  The caller owns all memory; the library borrows the
  *    pointers until the work it enqueued has finished, keeps no reference and
  *    never allocates device memory.
  *  - `stream` is a hipStream_t passed as void* (NULL = the null stream).  Work is
@@ -354,7 +355,7 @@ typedef struct cvx_rmsnorm_desc {
     int rows, c;        /* x [rows][c]; both at least 1, c at most 2^30          */
     int dtype;          /* CVX_DT_F32, _F16 or _BF16: x, residual, sum           */
     int out_dtype;      /* type of y: dtype, or CVX_DT_E4M3                      */
-    float eps;          /* > 0                                                   */
+    float eps;          /* > 0, finite                                           */
     long x_stride, res_stride, sum_stride, y_stride; /* row strides, 0 or >= c  */
 } cvx_rmsnorm_desc;
 

@@ -28,6 +28,7 @@ def norm(x=X, r=None, g=G, s=None, y=Y, q=None, **kw):
     (dict(dtype=E4M3), ARG), (dict(dtype=4), ARG), (dict(dtype=-1), ARG),
     (dict(out_dtype=F16), ARG), (dict(out_dtype=F32), ARG), (dict(out_dtype=7), ARG),
     (dict(eps=0.0), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG),
+    (dict(eps=float("inf")), ARG),
     (dict(x=None), NULL), (dict(g=None), NULL), (dict(y=None), NULL),
     (dict(out_dtype=E4M3), NULL),                            # 8 bits without scales
     (dict(x=X + 1), ALIGN), (dict(y=Y + 1), ALIGN), (dict(g=G + 2), ALIGN), (dict(r=R + 1), ALIGN),
