@@ -30,8 +30,8 @@
 // instructions: for every 32 tokens, each distinct adapter's rows of B, with v
 // as two 16-bit values (v = high + low, so v keeps 16 bits in bf16 and 21 in
 // fp16; k_lora_join makes them, or the tile itself); the lanes whose token names the adapter keep the
-// result.  fp16, whose range v may leave, takes v and the sums divided by a power
-// of two per token.
+// result.  fp16, whose range v may leave, takes v divided by a power of two per
+// token, and the product is added to the sums when it is whole.
 #include <stdio.h>
 
 #include "lin_common.h"
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
                         row[m] = ch < a.cout ? (unsigned)ch * (unsigned)a.rank * 2u + 16u * hi : kOOB;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            c[m][i] = V16<T>::BF ? acc[mh + m][n][i] : acc[mh + m][n][i] * down;
+                            c[m][i] = V16<T>::BF ? acc[mh + m][n][i] : 0.0f;
                     }
                     for (int r0 = 0; r0 < a.rank; r0 += 32) {
                         u32x4 b[2][2];
@@ -386,7 +386,9 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            acc[mh + m][n][i] = mine ? (V16<T>::BF ? c[m][i] : c[m][i] * up) : acc[mh + m][n][i];
+                            acc[mh + m][n][i] = !mine          ? acc[mh + m][n][i]
+                                                : V16<T>::BF ? c[m][i]
+                                                             : fmaf(c[m][i], up, acc[mh + m][n][i]);
                 }
             }
         }
