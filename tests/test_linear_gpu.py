@@ -304,6 +304,18 @@ def test_linear_low_rank_values_beyond_16_bits(t):
     c.check()
 
 
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("t", [20, 100])
+def test_linear_sums_beside_huge_low_rank_values(t, dt):
+    # channels whose rows of B are zero keep their sums, however large v is
+    c = Case(t, t, 128, 64, dt, False, 8, 3, ids="one")
+    c.alpha[:] = 1e37
+    c.b[:, :40] = 0
+    got = c.run()[:, :40]
+    want, tol = c.definition()
+    assert ((got - want[:, :40]).abs() <= tol[:, :40]).all()
+
+
 def test_linear_is_the_same_every_time():
     for t in (30, 150):
         c = Case(t, t, 1040, 132, BF16, False, 16, 7)
