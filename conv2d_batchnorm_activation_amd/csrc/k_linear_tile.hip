@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[mh + m][n][i] = apply_act_fast(acc[mh + m][n][i], decltype(act)::value);
+                        acc[mh + m][n][i] = apply_act_nan(acc[mh + m][n][i], decltype(act)::value);
             };
             if (a.res) {
 #pragma unroll

@@ -163,11 +163,18 @@ __device__ __forceinline__ void lora_parts(const float (&v)[8], u32x4& high, u32
     low = __builtin_bit_cast(u32x4, l);
 }
 
+// The activation of a projection.  A NaN stays one (what marks a token as bad passes
+// on), so ReLU is the maximum that keeps it, one instruction like the other one.
+__device__ __forceinline__ float apply_act_nan(float v, int act)
+{
+    return act == CVX_ACT_RELU ? __builtin_elementwise_maximum(v, 0.0f) : apply_act_fast(v, act);
+}
+
 // z (scale, bias, adapters in it) -> y
 __device__ __forceinline__ float finish(float z, float r, int act, int res_mode)
 {
     if (res_mode == CVX_RES_BEFORE_ACT) z += r;
-    z = apply_act_fast(z, act);
+    z = apply_act_nan(z, act);
     if (res_mode == CVX_RES_AFTER_ACT) z += r;
     return z;
 }

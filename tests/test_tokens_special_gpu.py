@@ -1,0 +1,62 @@
+"""Infinities and NaN through cvx_linear's epilogue: a NaN sum is a NaN output under
+every activation, in each of the kernels, and touches only the outputs whose
+definition holds it.  Finite outputs beside them keep the tolerance of their case."""
+import pytest
+import torch
+
+from test_linear_gpu import BF16, F16, NONE, RELU, SILU, Case
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+SHAPES = [
+    # tokens, c_in, c_out: one token; 8, 16, 32 and 64 a workgroup, of 16 and of 32 channels; blocks of 64
+    # (16 bits; tiles in 8); the three tiles
+    (1, 144, 100), (7, 144, 100), (12, 144, 100), (20, 144, 100), (60, 144, 100), (60, 64, 4100), (100, 2064, 132),
+    (100, 144, 100), (1000, 80, 4092), (4097, 48, 3588),
+]
+
+
+def setup_module(module):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def poison(c):
+    """Plants NaN and infinities in what the case reads."""
+    last = c.t - 1
+    if c.t > 3:
+        if c.x8:
+            c.x.view(torch.uint8)[last, 9] = 0x7f  # e4m3's NaN
+            c.sx[2] = NAN                          # a row that the norm marked
+        else:
+            c.x[last, 9] = NAN
+    c.bias[5] = NAN
+    c.bias[9] = -INF
+    c.bias[17] = INF
+    if c.res is not None:
+        c.res[0, 30] = NAN
+    if c.rank:
+        c.ids[0] = 1 if c.t > 1 else 0
+        c.a[2 % c.n, 3, 5] = NAN
+        c.b[2 % c.n, 40, 1] = INF
+
+
+@pytest.mark.parametrize("x8", [False, True], ids=["x16", "x8"])
+@pytest.mark.parametrize("act", [NONE, RELU, SILU], ids=["none", "relu", "silu"])
+@pytest.mark.parametrize("shape", SHAPES, ids=["x".join(map(str, s)) for s in SHAPES])
+def test_linear_keeps_nan_through_the_activation(shape, act, x8):
+    t, ci, co = shape
+    for dt, rank, res in ((BF16, 8, 1), (F16, 0, 0), (F16, 16, 2)):
+        c = Case(t + act + rank, t, ci, co, dt, x8, rank, 3 if rank else 0, act, res)
+        poison(c)
+        got = c.run()
+        want, tol = c.definition()
+        nan = torch.isnan(want)
+        assert nan.any() and not nan.all()
+        assert torch.equal(torch.isnan(got), nan), f"{c.plan}: NaN in other places than the definition's"
+        exact = ~nan & ~(torch.isfinite(want) & torch.isfinite(tol))
+        assert torch.equal(got[exact], want[exact]), f"{c.plan}: infinities"
+        rest = ~nan & ~exact
+        assert ((got - want).abs() <= tol)[rest].all(), c.plan
