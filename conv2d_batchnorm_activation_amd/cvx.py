@@ -147,7 +147,7 @@ def _check(st: int, where: str) -> None:
 
 def _ptr(t) -> Optional[int]:
     """Device (or raw) pointer of a tensor / int / None."""
-    if t is None or t.__class__ is int:
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -323,7 +323,7 @@ def make_rmsnorm_desc(rows, c, dtype, out_dtype=None, eps=1e-6, x_stride=0, res_
 
 def _gpu_ptr(t) -> Optional[int]:
     """_ptr of what an operator on tokens is given; host tensors are refused."""
-    if t is None or t.__class__ is int:
+    if t is None or isinstance(t, int):
         return t
     if not t.is_cuda:
         raise ValueError("tensors have to be on a GPU")
