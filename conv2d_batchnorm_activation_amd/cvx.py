@@ -2,8 +2,10 @@
 
 Every function here has the name of the C entry point it wraps and does nothing
 but turn tensors into device pointers, pick the caller's current HIP stream and
-turn status codes into exceptions.  All computation happens in libcvx's HIP
-kernels.  PyTorch provides device memory and streams.
+turn status codes into exceptions; the operators on tokens also run on their
+input's GPU and refuse (ValueError) operands elsewhere or of another element type
+than their descriptor's.  All computation happens in libcvx's HIP kernels.
+PyTorch provides device memory and streams.
 
 Importing this module raises ImportError when libcvx.so has not been built:
 there is no fallback path.
@@ -321,33 +323,65 @@ def make_rmsnorm_desc(rows, c, dtype, out_dtype=None, eps=1e-6, x_stride=0, res_
                             sum_stride, y_stride)
 
 
-def _gpu_ptr(t) -> Optional[int]:
-    """_ptr of what an operator on tokens is given; host tensors are refused."""
-    if t is None or isinstance(t, int):
-        return t
-    if not t.is_cuda:
-        raise ValueError("tensors have to be on a GPU")
+#: what an operand on tokens is held in, by its type in the descriptor; a type that is none of
+#: these is the library's to refuse
+_HELD = {CVX_DT_F32: torch.float32, CVX_DT_F16: torch.float16, CVX_DT_BF16: torch.bfloat16,
+         CVX_DT_E4M3: torch.float8_e4m3fn}
+_F32, _I32 = torch.float32, torch.int32
+
+
+def _operand(t, held, dev, name) -> Optional[int]:
+    """_ptr of what an operator on tokens is given.  Tensors in host memory, on another GPU than
+    the input (`dev`, None where that is an address) or of another element type than `held` (None:
+    any; e4m3 may be held as bytes) are refused: a kernel would read them as what they are not,
+    past their end where they are narrower."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is held and t.get_device() == dev >= 0:
+            return t.data_ptr()
+    except (AttributeError, TypeError):  # an address, or an input that is one
+        if isinstance(t, int):
+            return t
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name}: tensors have to be on a GPU")
+    if at != (torch.cuda.current_device() if dev is None else dev):
+        raise ValueError(f"{name}: tensors have to be on their input's GPU")
+    if held not in (None, t.dtype) and (held, t.dtype) != (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"{name}: {t.dtype}, where the call takes {held}")
     return t.data_ptr()
 
 
-def _elsewhere(x, call, *args) -> bool:
+def _device(x) -> Optional[int]:
+    """The device of an input: -1 in host memory, None for an address."""
+    return None if x is None or isinstance(x, int) else x.get_device()
+
+
+def _elsewhere(dev, call, *args) -> bool:
     """Operators on tokens run on their input's device: where that is not the current
     one, makes it current, calls again and says so."""
-    if not isinstance(x, torch.Tensor):
-        return False
-    dev = x.get_device()
-    if dev < 0 or dev == torch.cuda.current_device():
+    if dev is None or dev < 0 or dev == torch.cuda.current_device():
         return False
     with torch.cuda.device(dev):
         call(*args)
     return True
 
 
+def _stream_on(dev, stream) -> Optional[int]:
+    """_stream, where the current device is the input's."""
+    return _raw_stream(dev) if stream is None and dev is not None and _raw_stream is not None else _stream(stream)
+
+
 def cvx_rmsnorm(desc: cvx_rmsnorm_desc, x, residual, gamma, sum_out, y, y_scale=None, stream=None) -> None:
-    if _elsewhere(x, cvx_rmsnorm, desc, x, residual, gamma, sum_out, y, y_scale, stream):
+    dev = _device(x)
+    if _elsewhere(dev, cvx_rmsnorm, desc, x, residual, gamma, sum_out, y, y_scale, stream):
         return
-    _check(lib.cvx_rmsnorm(ctypes.byref(desc), _gpu_ptr(x), _gpu_ptr(residual), _gpu_ptr(gamma), _gpu_ptr(sum_out),
-                           _gpu_ptr(y), _gpu_ptr(y_scale), _stream(stream)), "cvx_rmsnorm")
+    held = _HELD.get(desc.dtype)
+    _check(lib.cvx_rmsnorm(ctypes.byref(desc), _operand(x, held, dev, "x"), _operand(residual, held, dev, "residual"),
+                           _operand(gamma, _F32, dev, "gamma"), _operand(sum_out, held, dev, "sum_out"),
+                           _operand(y, _HELD.get(desc.out_dtype), dev, "y"), _operand(y_scale, _F32, dev, "y_scale"),
+                           _stream_on(dev, stream)), "cvx_rmsnorm")
 
 
 def make_linear_desc(tokens, c_in, c_out, dtype, x_dtype=None, act=CVX_ACT_NONE, res_mode=CVX_RES_NONE, rank=0,
@@ -372,10 +406,15 @@ def cvx_linear(desc: cvx_linear_desc, x, w, y, x_scale=None, scale=None, bias=No
     if ws_bytes is None:
         ws_bytes = 0 if workspace is None or isinstance(workspace, int) else \
             workspace.numel() * workspace.element_size()
-    if _elsewhere(x, cvx_linear, desc, x, w, y, x_scale, scale, bias, residual, lora_a, lora_b, lora_alpha, lora_id,
+    dev = _device(x)
+    if _elsewhere(dev, cvx_linear, desc, x, w, y, x_scale, scale, bias, residual, lora_a, lora_b, lora_alpha, lora_id,
                   workspace, ws_bytes, stream):
         return
-    _check(lib.cvx_linear(ctypes.byref(desc), _gpu_ptr(x), _gpu_ptr(x_scale), _gpu_ptr(w), _gpu_ptr(scale),
-                          _gpu_ptr(bias), _gpu_ptr(residual), _gpu_ptr(lora_a), _gpu_ptr(lora_b),
-                          _gpu_ptr(lora_alpha), _gpu_ptr(lora_id), _gpu_ptr(y), _gpu_ptr(workspace), ws_bytes,
-                          _stream(stream)), "cvx_linear")
+    held, held_x = _HELD.get(desc.dtype), _HELD.get(desc.x_dtype)
+    _check(lib.cvx_linear(ctypes.byref(desc), _operand(x, held_x, dev, "x"), _operand(x_scale, _F32, dev, "x_scale"),
+                          _operand(w, held_x, dev, "w"), _operand(scale, _F32, dev, "scale"),
+                          _operand(bias, _F32, dev, "bias"), _operand(residual, held, dev, "residual"),
+                          _operand(lora_a, held, dev, "lora_a"), _operand(lora_b, held, dev, "lora_b"),
+                          _operand(lora_alpha, _F32, dev, "lora_alpha"), _operand(lora_id, _I32, dev, "lora_id"),
+                          _operand(y, held, dev, "y"), _operand(workspace, None, dev, "workspace"), ws_bytes,
+                          _stream_on(dev, stream)), "cvx_linear")
