@@ -16,6 +16,7 @@ constexpr long kMaxPitch = 1L << 21;   // row stride of a projection's operands:
 constexpr int kMaxChannels = 1 << 20;  // channels of a projection
 constexpr int kMaxNormed = 1 << 30;    // channels of a row that is normed: their index stays an int
 constexpr int kMaxTokens = 1 << 24;    // tokens of a projection
+constexpr long kMaxOut = 1L << 37;     // its outputs: 275 GB, and tiles of fewer than 2^32 threads in all
 
 inline bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -54,7 +55,7 @@ cvx_status check_linear(const cvx_linear_desc* d, long* xs, long* rs, long* ys)
     if (d->res_mode < CVX_RES_NONE || d->res_mode > CVX_RES_AFTER_ACT) return CVX_ERR_ARG;
     if (d->rank < 0 || d->n_adapters < 0 || (d->rank == 0) != (d->n_adapters == 0)) return CVX_ERR_ARG;
     if (d->tokens < 1 || d->c_in < 1 || d->c_out < 1 || d->tokens > kMaxTokens || d->c_in > kMaxChannels ||
-        d->c_out > kMaxChannels)
+        d->c_out > kMaxChannels || (long)d->tokens * d->c_out > kMaxOut)
         return CVX_ERR_SHAPE;
     if (!stride_of(d->x_stride, d->c_in, d->tokens, xs) || *xs > kMaxPitch) return CVX_ERR_SHAPE;
     if (!stride_of(d->y_stride, d->c_out, d->tokens, ys) || *ys > kMaxPitch) return CVX_ERR_SHAPE;

@@ -472,9 +472,7 @@ hipError_t launch_tile_t(LinArgs a, const LinPlan& p, hipStream_t s)
 {
     a.tiles_m = (a.cout + 64 * p.mb - 1) / (64 * p.mb);
     a.tiles_n = (a.tokens + 64 * p.nb - 1) / (64 * p.nb);
-    const long n = (long)a.tiles_m * a.tiles_n;
-    if (n > (1l << 22)) return hipErrorInvalidValue;  // a grid holds fewer than 2^32 threads
-    const dim3 grid((unsigned)n);
+    const dim3 grid((unsigned)((long)a.tiles_m * a.tiles_n));  // few enough: tokens * c_out is at most 2^37
     if (p.mb == 4)
         launch_tile_k<T, X8, 2, 4, 4, 2, 2>(a, grid, s);
     else if (p.nb == 2)

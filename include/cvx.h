@@ -391,7 +391,8 @@ CVX_API cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc *d, const void *x, const v
 
 typedef struct cvx_linear_desc {
     int tokens;         /* rows of x and y, 1 to 2^24                             */
-    int c_in, c_out;    /* channels, at most 2^20 each                            */
+    int c_in, c_out;    /* channels, at most 2^20 each; tokens * c_out at most 2^37,
+                         * and no operand more than 2^40 elements from first to last  */
     int dtype;          /* CVX_DT_F16 or _BF16: y, residual, adapters             */
     int x_dtype;        /* type of x and w: dtype, or CVX_DT_E4M3                 */
     int act;            /* CVX_ACT_*                                              */

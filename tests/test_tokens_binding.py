@@ -162,3 +162,40 @@ def test_an_input_on_another_gpu_is_made_current(taken, monkeypatch):
     norm_call(norm_operands(F16, F16, 1), F16, F16)
     linear_call(linear_operands(F16, F16, 1), F16, F16)
     assert len(taken) == 2 and now == [0]
+
+
+def tiles(d):
+    """(workgroups, threads of one) of the projection's launch for a descriptor."""
+    plan = cvx.cvx_linear_plan(d)
+    kind, size = plan.split()[1:3]
+    bm, bn = map(int, size.split("x"))
+    n = -(-d.c_out // bm) * -(-d.tokens // bn)
+    return n, 512 if kind == "few" or bm == 256 else 256
+
+
+@pytest.mark.parametrize("tokens,c_out", [(1 << 24, 1 << 20), (1 << 24, (1 << 13) + 4), ((1 << 17) + 1, 1 << 20)])
+def test_more_outputs_than_a_launch_takes(tokens, c_out):
+    # refused as a size, before the adapters' first product is enqueued
+    at = [(i + 1) << 50 for i in range(12)]
+    for rank in (0, 16):
+        d = cvx.make_linear_desc(tokens, 64, c_out, BF16, rank=rank, n_adapters=3 if rank else 0)
+        with pytest.raises(cvx.CvxError) as e:
+            cvx.cvx_linear(d, at[0], at[1], at[2], lora_a=at[3], lora_b=at[4], lora_id=at[5], workspace=at[6],
+                           ws_bytes=1 << 49)
+        assert e.value.status == -2
+        assert cvx.cvx_linear_workspace_bytes(d) == 0
+        with pytest.raises(cvx.CvxError):
+            cvx.cvx_linear_plan(d)
+
+
+def test_the_most_outputs_are_one_launch():
+    for c_in in (8, 64, 4096, 1 << 20):
+        for t in range(25):
+            for tokens in {1 << t, (1 << t) - 1, (1 << t) + 1, (1 << t) * 5 // 4 + 1}:
+                if not 1 <= tokens <= 1 << 24:
+                    continue
+                for c_out in {min(1 << 20, (1 << 37) // tokens) // 4 * 4, 4, 260, 516, 4100}:
+                    if tokens * c_out > 1 << 37 or tokens * c_in > 1 << 40:  # (no operand spans more)
+                        continue
+                    n, threads = tiles(cvx.make_linear_desc(tokens, c_in, c_out, BF16))
+                    assert n * threads < 1 << 32, (tokens, c_in, c_out)
