@@ -365,8 +365,11 @@ typedef struct cvx_rmsnorm_desc {
  *     h = x + residual                     (h = x without a residual)
  *     q = 1 / sqrt(mean_i(h_i^2) + eps)
  *     sum = h,  y_i = h_i * gamma_i * q    each rounded once to its type
- * h enters the norm in 32 bits, whatever its type; sums and products are taken in
- * 64 bits, so no finite row overflows them.  With out_dtype = CVX_DT_E4M3,
+ * h enters the norm as the fp32 sum of x and residual, whatever its type, and is an
+ * infinity where that overflows; squares, sums and products are taken in 64 bits, so
+ * no row whose h is finite overflows them.  One form is wider: of fp32 rows with a
+ * residual and 8-bit output h enters the norm in 64 bits, so that a code is the
+ * nearest to its value, and only `sum` can overflow.  With out_dtype = CVX_DT_E4M3,
  * u_i = h_i*gamma_i and t = max_i |u_i|,
  *     y_i = e4m3(u_i * (448/t)),  y_scale = t*q/448     (t = 0: zeros)
  * so that y_i * y_scale is the norm's output; q, which depends on the whole

@@ -1,10 +1,12 @@
-"""Infinities and NaN through cvx_linear's epilogue: a NaN sum is a NaN output under
-every activation, in each of the kernels, and touches only the outputs whose
-definition holds it.  Finite outputs beside them keep the tolerance of their case."""
+"""Infinities and NaN through the operators on tokens.  Through cvx_linear's epilogue: a
+NaN sum is a NaN output under every activation, in each of the kernels, and touches
+only the outputs whose definition holds it; finite outputs beside them keep the
+tolerance of their case.  Through cvx_rmsnorm: sums that leave fp32's range."""
 import pytest
 import torch
 
 from test_linear_gpu import BF16, F16, NONE, RELU, SILU, Case
+from test_rmsnorm_gpu import F32, compare, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +62,24 @@ def test_linear_keeps_nan_through_the_activation(shape, act, x8):
         assert torch.equal(got[exact], want[exact]), f"{c.plan}: infinities"
         rest = ~nan & ~exact
         assert ((got - want).abs() <= tol)[rest].all(), c.plan
+
+
+@pytest.mark.parametrize("c", [40, 5000, 30000])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_rmsnorm_sums_that_leave_fp32(dt, c):
+    # h is the fp32 sum of x and the residual, an infinity here, and so is `sum`; in the one
+    # form that takes h in 64 bits the row is like any other
+    x, r, g = inputs(c, 3, c, dt)
+    x[1] *= 2.0 ** 100
+    r[1] *= 2.0 ** 100
+    x[1, 7] = r[1, 7] = 3e38
+    fine = [0, 2]
+    for out8 in (False, True):
+        s, y, q = run(x, r, g, dt, out8)
+        compare(x[fine], r[fine], g, dt, out8, (s[fine], y[fine], q[fine]), "rows beside")
+        assert s[1, 7] == INF
+        if out8 and dt == F32:
+            compare(x, r, g, dt, out8, (s, y, q), "h in 64 bits")
+        else:
+            assert torch.isnan(y[1, 7]) and not y[1, :7].any() and not y[1, 8:].any()
+            assert torch.isnan(q[1]) or not out8
