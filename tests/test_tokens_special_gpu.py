@@ -5,10 +5,13 @@ tolerance of their case.  Through cvx_rmsnorm: sums that leave fp32's range."""
 import pytest
 import torch
 
-from test_linear_gpu import BF16, F16, NONE, RELU, SILU, Case
+from gpu_util import DEV, say
+from test_linear_gpu import BF16, E4M3, F16, NONE, RELU, SILU, Case
 from test_rmsnorm_gpu import F32, compare, inputs, run
 
 pytestmark = pytest.mark.gpu
+
+from conv2d_batchnorm_activation_amd import cvx  # noqa: E402
 
 NAN, INF = float("nan"), float("inf")
 
@@ -83,3 +86,34 @@ def test_rmsnorm_sums_that_leave_fp32(dt, c):
         else:
             assert torch.isnan(y[1, 7]) and not y[1, :7].any() and not y[1, 8:].any()
             assert torch.isnan(q[1]) or not out8
+
+
+@pytest.mark.parametrize("outliers", [1, 100], ids=["normal", "outliers"])
+@pytest.mark.parametrize("tokens", [64, 65, 1000, 4097], ids=["few", "tile128x64", "tile128x128", "tile256x256"])
+def test_linear_e4m3_sums_before_they_are_rounded(tokens, outliers):
+    # every token is the same and the bias takes its sum away, so that what comes out is the
+    # error of the sum itself.  Up to 64 tokens it is that of fp32 sums of exact products; beyond,
+    # of eight consecutive channels' products up to seven may each lose 2^-13 of the largest,
+    # itself at most the largest x times the largest w.  The bias is rounded to fp32, the output
+    # once.
+    ci, co, f = 1024, 3588, torch.float64
+    g = torch.Generator().manual_seed(outliers)
+    x = torch.randn(1, ci, generator=g) * 4
+    x[:, ::64] *= outliers
+    x = x.clamp(-448, 448).to(torch.float8_e4m3fn)
+    w = (torch.randn(co, ci, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    xd, wd = x.to(f), w.to(f)
+    z, mag = (xd @ wd.t())[0], (xd.abs() @ wd.abs().t())[0]
+    bias = (-z).float()
+    y = torch.full((tokens, co), NAN, dtype=torch.bfloat16, device=DEV)
+    d = cvx.make_linear_desc(tokens, ci, co, BF16, E4M3)
+    say(cvx.cvx_linear_plan(d))
+    cvx.cvx_linear(d, x.view(torch.uint8).repeat(tokens, 1).to(DEV), w.to(DEV), y, torch.ones(tokens, device=DEV), None,
+                   bias.to(DEV))
+    err = y.cpu().to(f) - (z + bias.to(f))[None, :]
+    tol = (ci + 2) * 2.0 ** -24 * mag
+    if tokens > 64:
+        tol = tol + 7 * 2.0 ** -13 * (xd.abs().view(-1, 8).amax(1) @ wd.abs().view(co, -1, 8).amax(2).t())
+    tol = tol * (1 + 2.0 ** -8)
+    say(f"error of the sums, of their size: {float(err.square().mean().sqrt() / z.square().mean().sqrt()):.3g}")
+    assert (err.abs() <= tol).all()
