@@ -20,7 +20,10 @@
 // 15.0 (4.5), with 16 adapters of rank 16 21.3; 48 tokens bf16, 4096 -> 8192 16.6
 // (4.0), with 32 adapters of rank 32 34.  A copy of such weights runs at 5.4 TB/s;
 // what is missing is a workgroup's first fetch and its end, as each compute unit
-// has one or two workgroups in all.
+// has one or two workgroups in all.  With a residual or adapters what the end needs
+// is loaded ahead of the first products (below), and only the stages fetched before
+// stand against that time: the 17 us between 34 and 16.6 are a launch for v, 5.4,
+// and 12 that the start and the end take longer.
 #include "lin_common.h"
 
 #include "cvx_internal.h"
@@ -204,8 +207,11 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     issue(1, st1);
     issue(2, st2);
     if constexpr (D == 4) issue(3, st3);
-    // What the end needs is loaded while the first stages are under way.  A thread
-    // finishes one channel (c) of every TSTEP-th token.
+    // What the end needs is loaded here, behind the first stages' fetches and ahead of
+    // the first products.  Loads return in their order, and each of the residual's, a
+    // 16-bit load behind a condition of its own, is waited for before the next; so a
+    // workgroup's products begin once all of it is there.  A thread finishes one
+    // channel (c) of every TSTEP-th token.
     constexpr int CH = 16 * RB, TSTEP = 64 * W / CH, ITEMS = (16 * NT + TSTEP - 1) / TSTEP;
     const int ch = tid % CH, tfirst = tid / CH, c = c0 + ch;
     const float sc = a.scale && c < a.cout ? a.scale[c] : 1.0f, bi = a.bias && c < a.cout ? a.bias[c] : 0.0f;

@@ -23,8 +23,7 @@
 // Measured: 16384 rows of 4096 bf16 channels with residual and sum to e4m3 86 us,
 // 5.4 TB/s, the rate of a copy of that size; 96 rows of 8192 fp16 channels 4.2 us
 // and one row of 4096 2.7 us, latency; 2048 rows of 20480 fp32 channels 135 us, 5.0
-// TB/s, 512 rows 39 us, 4.3 TB/s.  A row of 20480 by 512 threads instead of 1024:
-// 300 rows 20.7 us (23.9), 2048 rows 143 (135).
+// TB/s, 512 rows 39 us, 4.3 TB/s; 1024 rows of 16384 bf16 channels 32 us, 4.2 TB/s.
 #include "cvx_internal.h"
 #include "tokens.h"
 
@@ -312,7 +311,10 @@ hipError_t launch_t(const RmsArgs& a, hipStream_t s)
     // 1024 threads' (fewer loads one after another) where they do not.  bf16 with a
     // residual: 4096 channels, 1 row 2.3 us by 1024 threads, 2.5 by 256; 64 rows 3.3 and
     // 3.6; 512 rows 5.7 and 5.3; 2048 rows 15.3 and 13.0.  8192 channels: 256 rows 4.9
-    // and 5.7, 512 rows 8.2 and 8.5, 1024 rows 14.2 and 12.5.
+    // and 5.7, 512 rows 8.2 and 8.5, 1024 rows 14.2 and 12.5.  Rows of more than 1024
+    // vectors are 1024 threads' however many they are, for the sake of the many: by 512
+    // threads 2048 rows of 20480 fp32 channels take 143 us instead of 135, though 300
+    // take 20.7 instead of 23.9 and 517 44.5 instead of 46.5.
     constexpr int VEC = 16 / (int)sizeof(T);
     const long nvec = ((long)a.c + VEC - 1) / VEC;
     const bool few = a.rows <= (nvec <= 512 ? 256 : 512);

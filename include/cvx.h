@@ -421,12 +421,15 @@ CVX_API cvx_status cvx_linear_plan(const cvx_linear_desc *d, char *buf, int buf_
  *     y        = act(z [+ residual]) [+ residual]                      by d->res_mode
  * Products are accumulated in fp32 (with 8-bit operands and more than 64 tokens,
  * the matrix cores align the products of eight consecutive channels to the
- * largest of them and drop what lies 2^-13 below it), v is kept in fp32 between
- * its two products (more than 64 tokens: it may be taken as the sum of two 16-bit
- * values, to 2^-16 of the token's largest), and y is rounded once.  A token without an adapter is one whose id is negative or
- * not below n_adapters.  An adapter's values, infinities and NaN included, reach
- * the tokens that name it and no others.  A NaN stays NaN through every activation
- * (max(0, NaN) is NaN here, where the convolutions give 0).  Results do not depend on timing.
+ * largest of them and drop what lies 2^-13 below it: about 2^-16 of the result's
+ * size on normal values, 2^-14 with one channel in 64 a hundred times larger; who
+ * needs more keeps x and w in 16 bits), v is kept in fp32 between its two products
+ * (more than 64 tokens: it may be taken as the sum of two 16-bit values, to 2^-16 of
+ * the token's largest), and y is rounded once.  A token without an adapter is one
+ * whose id is negative or not below n_adapters.  An adapter's values, infinities and
+ * NaN included, reach the tokens that name it and no others.  A NaN stays NaN through
+ * every activation (max(0, NaN) is NaN here, where the convolutions give 0).  Results
+ * do not depend on timing.
  *   x          : device [tokens][c_in] of x_dtype, 16-byte aligned rows.
  *   x_scale    : device fp32 [tokens]; required iff x_dtype is CVX_DT_E4M3
  *                (cvx_rmsnorm's y and y_scale are such operands).
