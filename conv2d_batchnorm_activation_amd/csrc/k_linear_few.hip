@@ -208,10 +208,10 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     issue(2, st2);
     if constexpr (D == 4) issue(3, st3);
     // What the end needs is loaded here, behind the first stages' fetches and ahead of
-    // the first products.  Loads return in their order, and each of the residual's, a
-    // 16-bit load behind a condition of its own, is waited for before the next; so a
-    // workgroup's products begin once all of it is there.  A thread finishes one
-    // channel (c) of every TSTEP-th token.
+    // the first products.  Loads return in their order; each of the residual's, a 16-bit
+    // load behind a condition of its own, is waited for before the next, and v is joined
+    // from the newest.  So with these a workgroup's products begin once all of it is
+    // there.  A thread finishes one channel (c) of every TSTEP-th token.
     constexpr int CH = 16 * RB, TSTEP = 64 * W / CH, ITEMS = (16 * NT + TSTEP - 1) / TSTEP;
     const int ch = tid % CH, tfirst = tid / CH, c = c0 + ch;
     const float sc = a.scale && c < a.cout ? a.scale[c] : 1.0f, bi = a.bias && c < a.cout ? a.bias[c] : 0.0f;
