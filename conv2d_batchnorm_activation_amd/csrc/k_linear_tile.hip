@@ -15,9 +15,10 @@
 // Measured: 4096^3 bf16 105 to 114 us (1200 to 1310 TFLOP/s; the library's product
 // 99), the matrix pipes busy half of the cycles that 2.4 GHz would give; 8192 x 4096
 // x 14336 e4m3 386 to 402 us (2400 to 2490), 0.47.  512 tokens, 4096 -> 4096: 22 us,
-// 256 workgroups of one tile, the pipes busy 0.31: 84 MB come past the XCDs' caches for 38 MB of operands, 4 TB/s, and 24 KB a stage
-// of 0.28 us into every compute unit.  Tiles go in whole rounds of 256: 559 tokens
-// of 8048 -> 7436 are 531 tiles of 128x128, three rounds, 192 us, the pipes at 0.15.
+// 256 workgroups of one tile, the pipes busy 0.31: 84 MB come past the XCDs' caches
+// for 38 MB of operands, 4 TB/s, and 24 KB a stage of 0.28 us into every compute
+// unit.  Tiles go in whole rounds of 256: 559 tokens of 8048 -> 7436 are 531 tiles of
+// 128x128, three rounds, 192 us, the pipes at 0.15.
 //
 // 8-bit operands (e4m3) are the same bytes: a stage is 128 channels instead of
 // 64, and the 32x32x64 instruction takes two pieces a lane where the 16-bit
