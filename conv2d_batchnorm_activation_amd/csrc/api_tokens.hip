@@ -14,6 +14,7 @@ namespace {
 constexpr long kMaxSpan = 1L << 40;    // elements from an operand's first to its last
 constexpr long kMaxPitch = 1L << 21;   // row stride of a projection's operands: 256 rows stay below 2^31 bytes
 constexpr int kMaxChannels = 1 << 20;  // channels of a projection
+constexpr int kMaxI8 = (1 << 17) - 16; // of 8-bit integers: their sums, of up to 2^14 each, stay below 2^31
 constexpr int kMaxNormed = 1 << 30;    // channels of a row that is normed: their index stays an int
 constexpr int kMaxTokens = 1 << 24;    // tokens of a projection
 constexpr long kMaxOut = 1L << 37;     // its outputs: 275 GB, and tiles of fewer than 2^32 threads in all
@@ -21,7 +22,8 @@ constexpr long kMaxOut = 1L << 37;     // its outputs: 275 GB, and tiles of fewe
 inline bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 inline bool dtype16(int dt) { return dt == CVX_DT_F16 || dt == CVX_DT_BF16; }
-inline unsigned dt_bytes(int dt) { return dt == CVX_DT_F32 ? 4 : dt == CVX_DT_E4M3 ? 1 : 2; }
+inline bool dtype8(int dt) { return dt == CVX_DT_E4M3 || dt == CVX_DT_I8; }
+inline unsigned dt_bytes(int dt) { return dt == CVX_DT_F32 ? 4 : dtype8(dt) ? 1 : 2; }
 
 // A strided operand [rows][c] in bytes: [lo, hi).
 struct Span {
@@ -50,7 +52,7 @@ inline bool stride_of(long given, long c, long rows, long* out)
 cvx_status check_linear(const cvx_linear_desc* d, long* xs, long* rs, long* ys)
 {
     if (d == nullptr) return CVX_ERR_NULL;
-    if (!dtype16(d->dtype) || (d->x_dtype != d->dtype && d->x_dtype != CVX_DT_E4M3)) return CVX_ERR_ARG;
+    if (!dtype16(d->dtype) || (d->x_dtype != d->dtype && !dtype8(d->x_dtype))) return CVX_ERR_ARG;
     if (d->act < CVX_ACT_NONE || d->act > CVX_ACT_SILU) return CVX_ERR_ARG;
     if (d->res_mode < CVX_RES_NONE || d->res_mode > CVX_RES_AFTER_ACT) return CVX_ERR_ARG;
     if (d->rank < 0 || d->n_adapters < 0 || (d->rank == 0) != (d->n_adapters == 0)) return CVX_ERR_ARG;
@@ -63,7 +65,8 @@ cvx_status check_linear(const cvx_linear_desc* d, long* xs, long* rs, long* ys)
     if (d->res_mode != CVX_RES_NONE &&
         (!stride_of(d->res_stride, d->c_out, d->tokens, rs) || *rs > kMaxPitch))
         return CVX_ERR_SHAPE;
-    const int per = d->x_dtype == CVX_DT_E4M3 ? 16 : 8;
+    if (d->x_dtype == CVX_DT_I8 && d->c_in > kMaxI8) return CVX_ERR_SHAPE;
+    const int per = dtype8(d->x_dtype) ? 16 : 8;
     if (d->c_in % per != 0 || *xs % per != 0) return CVX_ERR_UNSUPPORTED;
     if (d->c_out % 4 != 0 || *ys % 4 != 0 || *rs % 4 != 0) return CVX_ERR_UNSUPPORTED;
     if (d->rank % 8 != 0 || d->rank > kLoraMaxRank) return CVX_ERR_UNSUPPORTED;
@@ -79,10 +82,10 @@ cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc* d, const void* x, const void* res
 {
     if (d == nullptr) return CVX_ERR_NULL;
     if (d->dtype != CVX_DT_F32 && !dtype16(d->dtype)) return CVX_ERR_ARG;
-    if (d->out_dtype != d->dtype && d->out_dtype != CVX_DT_E4M3) return CVX_ERR_ARG;
+    if (d->out_dtype != d->dtype && !dtype8(d->out_dtype)) return CVX_ERR_ARG;
     if (!(d->eps > 0.0f) || d->eps > FLT_MAX) return CVX_ERR_ARG;
     if (d->rows < 1 || d->c < 1 || d->c > kMaxNormed) return CVX_ERR_SHAPE;
-    const bool out8 = d->out_dtype == CVX_DT_E4M3;
+    const bool out8 = dtype8(d->out_dtype);
     RmsArgs a;
     a.rs = a.ss = d->c;
     if (!stride_of(d->x_stride, d->c, d->rows, &a.xs) || !stride_of(d->y_stride, d->c, d->rows, &a.ys) ||
@@ -114,7 +117,7 @@ cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc* d, const void* x, const void* res
     a.rows = d->rows;
     a.c = d->c;
     a.eps = d->eps;
-    a.out8 = out8;
+    a.held = held_of(d->dtype, d->out_dtype);
     return launch_rmsnorm(a, d->dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? CVX_OK : CVX_ERR_HIP;
 }
 
@@ -143,7 +146,7 @@ cvx_status cvx_linear(const cvx_linear_desc* d, const void* x, const float* x_sc
     LinArgs a;
     const cvx_status st = check_linear(d, &a.xs, &a.rs, &a.ys);
     if (st != CVX_OK) return st;
-    const bool x8 = d->x_dtype == CVX_DT_E4M3, lora = d->rank > 0;
+    const bool x8 = dtype8(d->x_dtype), lora = d->rank > 0;
     if (!x || !w || !y || (x8 && !x_scale)) return CVX_ERR_NULL;
     if (d->res_mode != CVX_RES_NONE && !residual) return CVX_ERR_NULL;
     if (lora && (!lora_a || !lora_b || !lora_id)) return CVX_ERR_NULL;
@@ -207,9 +210,10 @@ cvx_status cvx_linear(const cvx_linear_desc* d, const void* x, const float* x_sc
     a.slice_len = p.slice_len;
     a.tiles_m = a.tiles_n = 0;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (lora && !p.one && launch_lora_down(a, p, d->dtype, x8, s) != hipSuccess) return CVX_ERR_HIP;
+    const int held = held_of(d->dtype, d->x_dtype);
+    if (lora && !p.one && launch_lora_down(a, p, d->dtype, held, s) != hipSuccess) return CVX_ERR_HIP;
     if (p.join && launch_lora_join(a, d->dtype, s) != hipSuccess) return CVX_ERR_HIP;
-    const hipError_t e = p.few ? launch_linear_few(a, p, d->dtype, x8, s) : launch_linear_tile(a, p, d->dtype, x8, s);
+    const hipError_t e = p.few ? launch_linear_few(a, p, d->dtype, held, s) : launch_linear_tile(a, p, d->dtype, held, s);
     return e == hipSuccess ? CVX_OK : CVX_ERR_HIP;
 }
 

@@ -41,13 +41,16 @@ __device__ __forceinline__ float lane_move(float v)
 
 // 16x16 block, 64 bytes of k a row.  e4m3 values are widened to 16 bits, exactly:
 // the 8-bit matrix instructions drop what lies 2^-13 below the largest of eight
-// products, and here the stream of the weights leaves time for better.
-template <typename T, bool X8>
-__device__ __forceinline__ f32x4 mma_piece(u32x4 w, u32x4 x, f32x4 c)
+// products, and here the stream of the weights leaves time for better.  Sums of 8-bit
+// integers are integers.
+template <typename T, int X, typename S>
+__device__ __forceinline__ S mma_piece(u32x4 w, u32x4 x, S c)
 {
-    if constexpr (X8) {
-        c = mma16<T>(widen8<T>(u32x2{w[0], w[1]}), widen8<T>(u32x2{x[0], x[1]}), c);
-        return mma16<T>(widen8<T>(u32x2{w[2], w[3]}), widen8<T>(u32x2{x[2], x[3]}), c);
+    if constexpr (X == kXE4m3) {
+        c = mma16<T>(widen8<T, X>(u32x2{w[0], w[1]}), widen8<T, X>(u32x2{x[0], x[1]}), c);
+        return mma16<T>(widen8<T, X>(u32x2{w[2], w[3]}), widen8<T, X>(u32x2{x[2], x[3]}), c);
+    } else if constexpr (X == kXI8) {
+        return mma16_i8(w, x, c);
     } else {
         return mma16<T>(w, x, c);
     }
@@ -66,11 +69,14 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 // NT blocks of 16 tokens, of which XR rows (a multiple of eight) are loaded.  ONE:
 // a single token with an adapter of up to 16 ranks; the adapter's A goes along as
 // 16 more rows, in every workgroup, which for one token is less than a launch.
-template <typename T, bool X8, bool ONE, int W, int RB, int NT, int XR, int D>
+template <typename T, int X, bool ONE, int W, int RB, int NT, int XR, int D>
 __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
 {
     typedef typename V16<T>::v8 v8;
-    constexpr unsigned XB = X8 ? 1 : 2;
+    typedef typename std::conditional<X == kXI8, i32x4, f32x4>::type sum_t;
+    typedef typename std::conditional<X == kXI8, int, float>::type sum1_t;
+    constexpr bool Q = X != kX16;  // 8-bit operands, tokens' scales
+    constexpr unsigned XB = Q ? 1 : 2;
     constexpr int PER = 2 * RB + XR / 8 + (ONE ? 2 : 0);  // fetches of eight rows a stage
     constexpr int WB = 2048 * RB, AB = WB + 128 * XR, SB = 1024 * PER;  // a wave's stage: weights, x, A; bytes
     static_assert(D == 3 || D == 4, "stages under way");
@@ -89,7 +95,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     a.tokens = a.tokens - t0 < 16 * NT ? a.tokens - t0 : 16 * NT;
     a.x = static_cast<const char*>(a.x) + t0 * a.xs * XB;
     a.y = static_cast<T*>(a.y) + t0 * a.ys;
-    if (X8) a.x_scale += t0;
+    if (Q) a.x_scale += t0;
     if (a.res) a.res = static_cast<const T*>(a.res) + t0 * a.rs;
     if (a.rank) {
         a.lora_id += t0;
@@ -143,11 +149,11 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
                                                          live[r & 1] ? wo + 8 * r * cb + kb + piece[r & 1] : kOOB, 0, 0,
                                                          0);
     };
-    f32x4 acc[RB][NT];
+    sum_t acc[RB][NT];
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < NT; ++n) acc[r][n] = sum_t{0, 0, 0, 0};
     f32x4 low = {0.0f, 0.0f, 0.0f, 0.0f};
     // One stage: its operands to registers, its buffer to the stage D on, the products.
     auto stage = [&](int i, unsigned char* st) {
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
 #pragma unroll
             for (int r = 0; r < RB; ++r)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[r][n] = mma_piece<T, X8>(wv[s][r], xv[s][n], acc[r][n]);
+                for (int n = 0; n < NT; ++n) acc[r][n] = mma_piece<T, X>(wv[s][r], xv[s][n], acc[r][n]);
         if constexpr (ONE)
 #pragma unroll
             for (int s = 0; s < 2; ++s) low = mma16<T>(av[s], xv[s][0], low);
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     for (int k = 0; k < ITEMS; ++k) {
         const int t = tfirst + TSTEP * k;
         const bool ok = t < a.tokens && c < a.cout;
-        sx[k] = X8 && ok ? a.x_scale[t] : 1.0f;
+        sx[k] = Q && ok ? a.x_scale[t] : 1.0f;
         res[k] = a.res && ok ? static_cast<const T*>(a.res)[(long)t * a.rs + c] : (T)0.0f;
     }
     if (a.rank) {
@@ -276,9 +282,9 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no fetch is under way when the stages are used again
     __syncthreads();
     if (!ONE && a.rank && !beside) low_rank();
-    f32x4* red = reinterpret_cast<f32x4*>(st0);  // [wave][RB][NT][lane]
+    sum_t* red = reinterpret_cast<sum_t*>(st0);  // [wave][RB][NT][lane]
     static_assert(RB * NT * 1024 <= SB, "the sums fit a wave's stage");
-    const float* redf = reinterpret_cast<const float*>(st0);
+    const sum1_t* red1 = reinterpret_cast<const sum1_t*>(st0);
 #pragma unroll
     for (int r = 0; r < RB; ++r)
 #pragma unroll
@@ -312,51 +318,51 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     for (int k = 0; k < ITEMS; ++k) {
         const int t = tfirst + TSTEP * k;
         if (t >= a.tokens || c >= a.cout) continue;
-        float z = 0.0f;
+        sum1_t sum = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w)
-            z += redf[(((w * RB + (ch >> 4)) * NT + (t >> 4)) * 64 + ((ch & 15) >> 2) * 16 + (t & 15)) * 4 + (ch & 3)];
-        z = fmaf(X8 ? z * sx[k] : z, sc, bi);
+            sum += red1[(((w * RB + (ch >> 4)) * NT + (t >> 4)) * 64 + ((ch & 15) >> 2) * 16 + (t & 15)) * 4 + (ch & 3)];
+        float z = (float)sum;  // of integers: rounded once from 2^24 up
+        z = fmaf(Q ? z * sx[k] : z, sc, bi);
         if (a.rank) z += us[t * CH + ch];
         static_cast<T*>(a.y)[(long)t * a.ys + c] = (T)finish(z, (float)res[k], a.act, a.res_mode);
     }
 }
 
-template <typename T, bool X8, int W, int RB, int NT, int XR, int D, bool ONE = false>
+template <typename T, int X, int W, int RB, int NT, int XR, int D, bool ONE = false>
 void launch_few_k(const LinArgs& a, hipStream_t s)
 {
     const dim3 grid((unsigned)((a.cout + 16 * RB - 1) / (16 * RB)), (unsigned)((a.tokens + 16 * NT - 1) / (16 * NT)));
-    hipLaunchKernelGGL((k_linear_few<T, X8, ONE, W, RB, NT, XR, D>), grid, dim3(64 * W), 0, s, a);
+    hipLaunchKernelGGL((k_linear_few<T, X, ONE, W, RB, NT, XR, D>), grid, dim3(64 * W), 0, s, a);
 }
 
-template <typename T, bool X8>
+template <typename T, int X>
 hipError_t launch_few_t(const LinArgs& a, const LinPlan& p, hipStream_t s)
 {
-    if constexpr (!X8) {
+    if constexpr (X == kX16) {
         if (p.one) {
-            launch_few_k<T, X8, 8, 1, 1, 8, 3, true>(a, s);
+            launch_few_k<T, X, 8, 1, 1, 8, 3, true>(a, s);
             return hipGetLastError();
         }
     }
     if (a.tokens <= 8)
-        launch_few_k<T, X8, 8, 1, 1, 8, 4>(a, s);
+        launch_few_k<T, X, 8, 1, 1, 8, 4>(a, s);
     else if (p.nt == 1)
-        launch_few_k<T, X8, 8, 1, 1, 16, 4>(a, s);
+        launch_few_k<T, X, 8, 1, 1, 16, 4>(a, s);
     else if (p.nt == 2)
-        launch_few_k<T, X8, 4, 1, 2, 32, 4>(a, s);
+        launch_few_k<T, X, 4, 1, 2, 32, 4>(a, s);
     else if (p.rb == 1)
-        launch_few_k<T, X8, 4, 1, 4, 64, 3>(a, s);
+        launch_few_k<T, X, 4, 1, 4, 64, 3>(a, s);
     else
-        launch_few_k<T, X8, 4, 2, 4, 64, 3>(a, s);
+        launch_few_k<T, X, 4, 2, 4, 64, 3>(a, s);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s)
+hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s)
 {
-    if (dtype == CVX_DT_F16) return x8 ? launch_few_t<half_t, true>(a, p, s) : launch_few_t<half_t, false>(a, p, s);
-    return x8 ? launch_few_t<bf16_t, true>(a, p, s) : launch_few_t<bf16_t, false>(a, p, s);
+    return by_types(dtype, held, [&](auto t, auto x) { return launch_few_t<typename decltype(t)::type, x.value>(a, p, s); });
 }
 
 }  // namespace cvx

@@ -3,14 +3,9 @@
 //
 // The weights are the A operand (rows = output channels) and the tokens the B
 // operand (columns = tokens), so a lane's accumulators are channels of one
-// token.  A stage is 128 bytes of every row of both operands, loaded straight
-// into LDS; the 16-byte pieces of a row are permuted by the row's index as they
-// are fetched, so that the lanes of an operand read (32 rows, the same piece) fall
-// in different banks while every fetch still takes whole 128-byte lines.  Stage
-// s+1 (and, with four stage buffers, up to s+3) arrives while s is multiplied; a
-// stage has one barrier, before which a wave waits for its own fetches of the next
-// stage only, and which drains nothing: a fence there waited for every fetch under
-// way (512 tokens, 4096 -> 4096 channels, 34 us instead of 22).
+// token (lin_tile.h has the loop).  A stage's barrier drains nothing: a fence there
+// waited for every fetch under way (512 tokens, 4096 -> 4096 channels, 34 us instead
+// of 22).
 //
 // Measured: 4096^3 bf16 105 to 114 us (1200 to 1310 TFLOP/s; the library's product
 // 99), the matrix pipes busy half of the cycles that 2.4 GHz would give; 8192 x 4096
@@ -42,7 +37,7 @@
 // token, and the product is added to the sums when it is whole.
 #include <stdio.h>
 
-#include "lin_common.h"
+#include "lin_tile.h"
 
 #include "cvx_internal.h"
 
@@ -50,37 +45,20 @@ namespace cvx {
 
 namespace {
 
-// Orders this wave's LDS accesses (which the hardware keeps in order) for the compiler.
-__device__ __forceinline__ void wave_lds_order()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
-}
-
-template <bool X8>
-struct Op {
-    typedef typename std::conditional<X8, i32x8, u32x4>::type type;
-};
-
 // WM x WN waves, each MB x NB blocks of 32 x 32; D stage buffers.
-template <typename T, bool X8, bool LORA, int WM, int WN, int MB, int NB, int D>
+template <typename T, int X, bool LORA, int WM, int WN, int MB, int NB, int D>
 __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(LinArgs a)
 {
-    typedef typename V16<T>::v4 v4;
-    typedef typename Op<X8>::type op_t;
-    constexpr unsigned XB = X8 ? 1 : 2;
-    constexpr int W = WM * WN, NT = 64 * W;
-    constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
-    constexpr int FM = BM / (8 * W), FN = BN / (8 * W);  // fetches of eight rows a wave, per stage and operand
-    constexpr int STEPS = X8 ? 2 : 4;
-    constexpr int SB = (BM + BN) * 128;  // bytes of a stage
-    static_assert(D == 2 || D == 4, "stage buffers");
-    static_assert(W * 4096 <= SB && MB % 2 == 0, "LDS is used again after the main loop");
+    typedef Tile<T, X, WM, WN, MB, NB, D> tile;
+    typedef typename tile::v4 v4;
+    constexpr bool Q = X != kX16;  // 8-bit operands, tokens' scales
+    constexpr unsigned XB = tile::XB;
+    constexpr int NT = tile::NT, BM = tile::BM, BN = tile::BN, SB = tile::SB;
     // an array a stage, so that waits are for the stage read, not for every fetch
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[SB], buf1[SB], buf2[D == 4 ? SB : 16],
         buf3[D == 4 ? SB : 16];
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
-    __shared__ float sx_lds[X8 ? BN : 1];
+    __shared__ float sx_lds[Q ? BN : 1];
     __shared__ int id_lds[LORA ? BN : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -105,115 +83,18 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
     const unsigned cb = (unsigned)a.cin * XB, pitch = (unsigned)a.xs * XB;
     const int mrows = a.cout - m0 < BM ? a.cout - m0 : BM;
     const int nrows = a.tokens - n0 < BN ? a.tokens - n0 : BN;
-    const char* wt = static_cast<const char*>(a.w) + (long)m0 * cb;
-    const char* xt = static_cast<const char*>(a.x) + (long)n0 * pitch;
-    const int nst = (int)((cb + 127) / 128);
-
-    // A fetch is eight rows of 128 bytes, eight lanes a row.  Rows past the operand
-    // are past the range of its descriptor, pieces past the end of a row are sent
-    // there.  The 16-byte pieces of row r lie permuted, piece p at p ^ (r/2 % 8): the
-    // sixteen lanes of an operand read that go together (0-3, 12-15, 20-27 of 32,
-    // or the others) then fall in all of the banks.
-    static_assert(W % 2 == 0, "a wave's fetches begin at rows 8 * wave + 16 * i");
-    const unsigned piece = (unsigned)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
-    static_assert(FM <= 8 && FN <= 8, "fetches a wave");
-    unsigned wo[8], xo[8];
+    TileRows op;
+    op.w = static_cast<const char*>(a.w) + (long)m0 * cb;
+    op.x = static_cast<const char*>(a.x) + (long)n0 * pitch;
+    op.wend = (unsigned)mrows * cb;
+    op.xend = (unsigned)(nrows - 1) * pitch + cb;
+    // rows past the operand are past its range
 #pragma unroll
-    for (int i = 0; i < FM; ++i) wo[i] = (unsigned)(8 * (wave + W * i) + (lane >> 3)) * cb + piece;
+    for (int i = 0; i < tile::FM; ++i)
+        op.wo[i] = (unsigned)tile::fetch_row(wave, lane, i) * cb + tile::piece(wave, lane);
 #pragma unroll
-    for (int i = 0; i < FN; ++i) xo[i] = (unsigned)(8 * (wave + W * i) + (lane >> 3)) * pitch + piece;
-    auto issue = [&](int st, unsigned char* buf) {
-        const unsigned kb = (unsigned)st * 128 < cb ? (unsigned)st * 128 : 0u;  // past the end: nothing is live
-        const unsigned dead = (unsigned)st * 128 + piece < cb ? 0u : kOOB;
-        const char *wk = wt + kb, *xk = xt + kb;
-        const unsigned wleft = (unsigned)mrows * cb - kb, xleft = (unsigned)(nrows - 1) * pitch + cb - kb;
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wk, wleft), (lds_void*)(buf + 1024 * (wave + W * i)), 16,
-                                                     wo[i] | dead, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xk, xleft),
-                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16,
-                                                     xo[i] | dead, 0, 0, 0);
-    };
-    unsigned slot[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) slot[s] = (unsigned)(l32 * 128 + (((2 * s + hi) ^ ((l32 >> 1) & 7)) * 16));
-    auto read = [&](const unsigned char* buf, int st, op_t (&A)[MB], op_t (&B)[NB]) {
-        const unsigned char* pa = buf + wm * MB * 4096;
-        const unsigned char* pb = buf + BM * 128 + wn * NB * 4096;
-        auto one = [&](const unsigned char* p) {
-            if constexpr (X8) {
-                const u32x4 x = *reinterpret_cast<const u32x4*>(p + slot[2 * st]);
-                const u32x4 y = *reinterpret_cast<const u32x4*>(p + slot[2 * st + 1]);
-                i32x8 o;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[e] = (int)x[e];
-                    o[4 + e] = (int)y[e];
-                }
-                return o;
-            } else {
-                return *reinterpret_cast<const u32x4*>(p + slot[st]);
-            }
-        };
-#pragma unroll
-        for (int n = 0; n < NB; ++n) B[n] = one(pb + 4096 * n);
-#pragma unroll
-        for (int m = 0; m < MB; ++m) A[m] = one(pa + 4096 * m);
-    };
-
-    f32x16 acc[MB][NB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
-    auto mul = [&](const op_t (&A)[MB], const op_t (&B)[NB]) {
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                if constexpr (X8)
-                    acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A[m], B[n], acc[m][n], 0, 0, 0,
-                                                                                0x7f7f7f7f, 0, 0x7f7f7f7f);
-                else
-                    acc[m][n] = mma32<T>(A[m], B[n], acc[m][n]);
-            }
-    };
-    // Orders a step's instructions: the reads of the next operands and the fetches
-    // of a later stage between the matrix instructions.
-    auto mix = [&](auto fetches) {
-        constexpr int READS = (X8 ? 2 : 1) * (MB + NB), MUL = MB * NB, F = decltype(fetches)::value;
-        constexpr int OTHER = READS + F;
-#pragma unroll
-        for (int i = 0; i < MUL; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-#pragma unroll
-            for (int o = i * OTHER / MUL; o < (i + 1) * OTHER / MUL; ++o) {
-                if (o < READS)
-                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                else
-                    __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
-            }
-        }
-    };
-    auto mix_all = [&]() {  // the same for a whole stage
-        constexpr int READS = (X8 ? 2 : 1) * (MB + NB) * STEPS, MUL = MB * NB * STEPS, OTHER = READS + FM + FN;
-#pragma unroll
-        for (int i = 0; i < MUL; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-#pragma unroll
-            for (int o = i * OTHER / MUL; o < (i + 1) * OTHER / MUL; ++o) {
-                if (o % (OTHER / (FM + FN)) == 0)
-                    __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
-                else
-                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-        }
-    };
+    for (int i = 0; i < tile::FN; ++i)
+        op.xo[i] = (unsigned)tile::fetch_row(wave, lane, i) * pitch + tile::piece(wave, lane);
     for (int i = tid; i < BM; i += NT) {
         const bool ok = m0 + i < a.cout;
         sc_lds[i] = !a.scale ? 1.0f : ok ? a.scale[m0 + i] : 0.0f;
@@ -221,77 +102,11 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
     }
     for (int i = tid; i < BN; i += NT) {
         const int token = n0 + i;
-        if (X8) sx_lds[i] = token < a.tokens ? a.x_scale[token] : 0.0f;
+        if (Q) sx_lds[i] = token < a.tokens ? a.x_scale[token] : 0.0f;
         if (LORA) id_lds[i] = adapter_of(a, token);
     }
-    // Both loops take D stages; those past the last are zeros, and so are the fetches past it.
-    typedef std::integral_constant<int, FM + FN> fetch;
-    if constexpr (D == 2) {
-        // A step's operands are read under the step before.
-        typedef std::integral_constant<int, 0> no_fetch;
-        op_t A0[MB], B0[NB], A1[MB], B1[NB];
-        auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
-#pragma unroll
-            for (int s = 0; s + 1 < STEPS; ++s) {
-                if (s & 1) {
-                    read(cur, s + 1, A0, B0);
-                    mul(A1, B1);
-                } else {
-                    read(cur, s + 1, A1, B1);
-                    mul(A0, B0);
-                }
-                mix(no_fetch());
-            }
-            wait_arrived<0>();  // the next stage has arrived, this wave has read the current one
-            stage_barrier();
-            issue(st + 2, cur);
-            read(nxt, 0, A0, B0);
-            mul(A1, B1);
-            mix(fetch());
-        };
-        issue(0, buf0);
-        wait_arrived<0>();
-        stage_barrier();
-        issue(1, buf1);
-        read(buf0, 0, A0, B0);
-        for (int st = 0; st < nst; st += 2) {
-            stage(st, buf0, buf1);
-            stage(st + 1, buf1, buf0);
-        }
-    } else {
-        // One wave a SIMD: a stage's operands are all read under the stage before, as
-        // a step's products (four instructions) are shorter than a read takes.
-        op_t A0[STEPS][MB], B0[STEPS][NB], A1[STEPS][MB], B1[STEPS][NB];
-        auto read_all = [&](const unsigned char* buf, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB]) {
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) read(buf, s, A[s], B[s]);
-        };
-        auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB],
-                         op_t(&An)[STEPS][MB], op_t(&Bn)[STEPS][NB]) {
-            wait_arrived<2 * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
-            stage_barrier();
-            issue(st + 4, cur);
-            read_all(nxt, An, Bn);
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) mul(A[s], B[s]);
-            mix_all();
-        };
-        issue(0, buf0);
-        issue(1, buf1);
-        issue(2, buf2);
-        issue(3, buf3);
-        wait_arrived<3 * (FM + FN)>();
-        stage_barrier();
-        read_all(buf0, A0, B0);
-        for (int st = 0; st < nst; st += 4) {
-            stage(st, buf0, buf1, A0, B0, A1, B1);
-            stage(st + 1, buf1, buf2, A1, B1, A0, B0);
-            stage(st + 2, buf2, buf3, A0, B0, A1, B1);
-            stage(st + 3, buf3, buf0, A1, B1, A0, B0);
-        }
-    }
-    wait_arrived<0>();  // no fetch is under way when LDS is used again
-    stage_barrier();
+    typename tile::sum_t total[MB][NB];
+    tile::sums(op, cb, wave, lane, buf0, buf1, buf2, buf3, total);
 
     // 32 tokens at a time; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one
     // token.  A load waits for the stores before it, so finished values are kept,
@@ -302,10 +117,11 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
                                   a.res ? (unsigned)((nrows - 1) * a.rs + a.cout) * 2u : 0u);
     const rsrc_t ry = make_rsrc(static_cast<T*>(a.y) + (long)n0 * a.ys, (unsigned)((nrows - 1) * a.ys + a.cout) * 2u);
     v4 out[NB][MB][4];
+    f32x16 acc[MB][NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
         const int t = (wn * NB + n) * 32 + l32;
-        const float sx = X8 ? sx_lds[t] : 1.0f;
+        const float sx = Q ? sx_lds[t] : 1.0f;
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -315,8 +131,8 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
                 const f32x4 bi = *reinterpret_cast<const f32x4*>(bi_lds + c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float z = acc[m][n][4 * j + i];
-                    acc[m][n][4 * j + i] = fmaf(X8 ? z * sx : z, sc[i], bi[i]);
+                    const float z = (float)total[m][n][4 * j + i];  // of integers: rounded once from 2^24 up
+                    acc[m][n][4 * j + i] = fmaf(Q ? z * sx : z, sc[i], bi[i]);
                 }
             }
 
@@ -440,62 +256,38 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    unsigned char* turn = buf0 + wave * 4096;
-    const int p = lane & 7;
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int m = 0; m < MB; m += 2) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<v4*>(turn + l32 * 128 + ((k ^ (l32 & 7)) * 16) + 8 * hi) = out[n][m + k / 4][k % 4];
-            wave_lds_order();
-            const int c = m0 + (wm * MB + m) * 32 + 8 * p;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tt = 8 * i + (lane >> 3), t = (wn * NB + n) * 32 + tt;
-                const u32x4 q = *reinterpret_cast<const u32x4*>(turn + tt * 128 + ((p ^ (tt & 7)) * 16));
-                const unsigned off = ((unsigned)t * (unsigned)a.ys + (unsigned)c) * 2u;
-                const bool live = t < nrows;
-                __builtin_amdgcn_raw_buffer_store_b128(q, ry, live && c + 8 <= a.cout ? (int)off : (int)kOOB, 0, 0);
-                if (a.cout & 4)  // the last four channels of a row
-                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{q[0], q[1]}, ry,
-                                                          live && c + 4 == a.cout ? (int)off : (int)kOOB, 0, 0);
-            }
-            wave_lds_order();
-        }
+    tile::store(out, buf0, wave, lane, ry, nrows, (unsigned)a.ys, m0, a.cout);
 }
 
-template <typename T, bool X8, int WM, int WN, int MB, int NB, int D>
+template <typename T, int X, int WM, int WN, int MB, int NB, int D>
 void launch_tile_k(const LinArgs& a, dim3 grid, hipStream_t s)
 {
     if (a.rank)
-        hipLaunchKernelGGL((k_linear_tile<T, X8, true, WM, WN, MB, NB, D>), grid, dim3(64 * WM * WN), 0, s, a);
+        hipLaunchKernelGGL((k_linear_tile<T, X, true, WM, WN, MB, NB, D>), grid, dim3(64 * WM * WN), 0, s, a);
     else
-        hipLaunchKernelGGL((k_linear_tile<T, X8, false, WM, WN, MB, NB, D>), grid, dim3(64 * WM * WN), 0, s, a);
+        hipLaunchKernelGGL((k_linear_tile<T, X, false, WM, WN, MB, NB, D>), grid, dim3(64 * WM * WN), 0, s, a);
 }
 
-template <typename T, bool X8>
+template <typename T, int X>
 hipError_t launch_tile_t(LinArgs a, const LinPlan& p, hipStream_t s)
 {
     a.tiles_m = (a.cout + 64 * p.mb - 1) / (64 * p.mb);
     a.tiles_n = (a.tokens + 64 * p.nb - 1) / (64 * p.nb);
     const dim3 grid((unsigned)((long)a.tiles_m * a.tiles_n));  // few enough: tokens * c_out is at most 2^37
     if (p.mb == 4)
-        launch_tile_k<T, X8, 2, 4, 4, 2, 2>(a, grid, s);
+        launch_tile_k<T, X, 2, 4, 4, 2, 2>(a, grid, s);
     else if (p.nb == 2)
-        launch_tile_k<T, X8, 2, 2, 2, 2, 4>(a, grid, s);
+        launch_tile_k<T, X, 2, 2, 2, 2, 4>(a, grid, s);
     else
-        launch_tile_k<T, X8, 2, 2, 2, 1, 4>(a, grid, s);
+        launch_tile_k<T, X, 2, 2, 2, 1, 4>(a, grid, s);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s)
+hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s)
 {
-    if (dtype == CVX_DT_F16) return x8 ? launch_tile_t<half_t, true>(a, p, s) : launch_tile_t<half_t, false>(a, p, s);
-    return x8 ? launch_tile_t<bf16_t, true>(a, p, s) : launch_tile_t<bf16_t, false>(a, p, s);
+    return by_types(dtype, held, [&](auto t, auto x) { return launch_tile_t<typename decltype(t)::type, x.value>(a, p, s); });
 }
 
 LinPlan linear_plan(const cvx_linear_desc& d)
@@ -532,7 +324,7 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     const struct {
         int mb, nb, stage, rest;
     } tiles[] = {{4, 4, 150, 1000}, {2, 2, 45, 500}, {2, 1, 28, 400}};
-    const long stages = ((long)d.c_in * (d.x_dtype == CVX_DT_E4M3 ? 1 : 2) + 127) / 128;
+    const long stages = ((long)d.c_in * (d.x_dtype == d.dtype ? 2 : 1) + 127) / 128;
     long best = -1;
     for (const auto& t : tiles) {
         const long n = (long)((d.c_out + 64 * t.mb - 1) / (64 * t.mb)) * ((d.tokens + 64 * t.nb - 1) / (64 * t.nb));
@@ -574,19 +366,19 @@ LinPlan linear_plan(const cvx_linear_desc& d)
 void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int len)
 {
     const char* t = d.dtype == CVX_DT_F16 ? "_Float16" : "__bf16";
-    const char* x8 = d.x_dtype == CVX_DT_E4M3 ? "true" : "false";
+    const int held = held_of(d.dtype, d.x_dtype);
     char lora[64] = "";
     if (p.one)
         snprintf(lora, sizeof lora, " rank=%d", d.rank);
     else if (d.rank)
         snprintf(lora, sizeof lora, " rank=%d slices=%d", d.rank, p.slices);
     if (p.few)
-        snprintf(buf, len, "linear few %dx%d%s kernel=cvx::k_linear_few<%s, %s, %s, %d, %d, %d, %d, %d>", 16 * p.rb,
-                 16 * p.nt, lora, t, x8, p.one ? "true" : "false", p.nt == 1 ? 8 : 4, p.rb, p.nt,
+        snprintf(buf, len, "linear few %dx%d%s kernel=cvx::k_linear_few<%s, %d, %s, %d, %d, %d, %d, %d>", 16 * p.rb,
+                 16 * p.nt, lora, t, held, p.one ? "true" : "false", p.nt == 1 ? 8 : 4, p.rb, p.nt,
                  d.tokens <= 8 ? 8 : 16 * p.nt, p.nt == 4 || p.one ? 3 : 4);
     else
-        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %s, %s, 2, %d, %d, %d, %d>", 64 * p.mb, 64 * p.nb,
-                 lora, t, x8, d.rank ? "true" : "false", p.mb == 4 ? 4 : 2, p.mb, p.mb == 4 ? 2 : p.nb,
+        snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %d, %s, 2, %d, %d, %d, %d>", 64 * p.mb, 64 * p.nb,
+                 lora, t, held, d.rank ? "true" : "false", p.mb == 4 ? 4 : 2, p.mb, p.mb == 4 ? 2 : p.nb,
                  p.mb == 4 ? 2 : 4);
 }
 

@@ -37,10 +37,11 @@ __device__ __forceinline__ int xcd_run(unsigned block, unsigned blocks)
 }
 
 // A block is 16 tokens, or a single one (NB = 0).
-template <typename T, bool X8, int NB>
+template <typename T, int X, int NB>
 __global__ void __launch_bounds__(256) k_lora_down(LinArgs a)
 {
     constexpr int TOK = NB ? 16 : 1;
+    constexpr bool X8 = X != kX16;       // e4m3 or integers: exact in 16 bits
     constexpr unsigned XB = X8 ? 1 : 2;  // bytes of an x value
     __shared__ f32x4 red[4][64];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(256) k_lora_down(LinArgs a)
             const int k = k0 + 32 * s + 8 * q;
             const unsigned off = k < a.cin && xrow != kOOB ? xrow + (unsigned)k * XB : kOOB;
             if constexpr (X8)
-                xv[s] = widen8<T>(bload64(rx, off));
+                xv[s] = widen8<T, X>(bload64(rx, off));
             else
                 xv[s] = bload128(rx, off);
         }
@@ -111,9 +112,10 @@ __global__ void __launch_bounds__(256) k_lora_down(LinArgs a)
 // many passes.  What the registers'
 // form above pays is the address unit: 16 rows a load are 64 cycles of it for
 // 1 KB, where a fetch of whole lines is 16.
-template <typename T, bool X8, int RB>
+template <typename T, int X, int RB>
 __global__ void __launch_bounds__(256) k_lora_down_many(LinArgs a)
 {
+    constexpr bool X8 = X != kX16;
     constexpr unsigned XB = X8 ? 1 : 2;
     constexpr int KS = X8 ? 128 : 64;                  // channels a stage
     constexpr int AL = X8 ? 2 : 1;                     // 128-byte lines of a row of A a stage
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(256) k_lora_down_many(LinArgs a)
             if (any) {
 #pragma unroll
                 for (int s = 0; s < 2 * AL; ++s) {
-                    const u32x4 x = X8 ? widen8<T>(u32x2{xv[s / AL][2 * (s % AL)], xv[s / AL][2 * (s % AL) + 1]}) : xv[s / AL];
+                    const u32x4 x = X8 ? widen8<T, X>(u32x2{xv[s / AL][2 * (s % AL)], xv[s / AL][2 * (s % AL) + 1]}) : xv[s / AL];
 #pragma unroll
                     for (int r = 0; r < RB; ++r) c[r] = mma16<T>(av[s][r], x, c[r]);
                 }
@@ -251,22 +253,22 @@ __global__ void __launch_bounds__(256) k_lora_join(LinArgs a)
     }
 }
 
-template <typename T, bool X8>
+template <typename T, int X>
 hipError_t launch_down_t(const LinArgs& a, const LinPlan& p, hipStream_t s)
 {
     const int tok = p.down_nb ? 16 * p.down_nb : 1;
     const dim3 grid((unsigned)((a.tokens + tok - 1) / tok), (unsigned)a.slices,
                     (unsigned)((a.rank + 16 * p.down_rc - 1) / (16 * p.down_rc)));
     if (p.down_nb == 0)
-        hipLaunchKernelGGL((k_lora_down<T, X8, 0>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_lora_down<T, X, 0>), grid, dim3(256), 0, s, a);
     else if (p.down_nb == 1)
-        hipLaunchKernelGGL((k_lora_down<T, X8, 1>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_lora_down<T, X, 1>), grid, dim3(256), 0, s, a);
     else if (p.down_rc == 1)
-        hipLaunchKernelGGL((k_lora_down_many<T, X8, 1>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_lora_down_many<T, X, 1>), grid, dim3(256), 0, s, a);
     else if (p.down_rc == 2)
-        hipLaunchKernelGGL((k_lora_down_many<T, X8, 2>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_lora_down_many<T, X, 2>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((k_lora_down_many<T, X8, 4>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_lora_down_many<T, X, 4>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -284,10 +286,9 @@ hipError_t launch_lora_join(const LinArgs& a, int dtype, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_lora_down(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s)
+hipError_t launch_lora_down(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s)
 {
-    if (dtype == CVX_DT_F16) return x8 ? launch_down_t<half_t, true>(a, p, s) : launch_down_t<half_t, false>(a, p, s);
-    return x8 ? launch_down_t<bf16_t, true>(a, p, s) : launch_down_t<bf16_t, false>(a, p, s);
+    return by_types(dtype, held, [&](auto t, auto x) { return launch_down_t<typename decltype(t)::type, x.value>(a, p, s); });
 }
 
 }  // namespace cvx

@@ -2,7 +2,8 @@
 // output, the row's scale, in one pass over the data.
 //
 //     h = x + r,  q = 1/sqrt(mean(h^2) + eps),  y = h*gamma*q
-//     8 bits: u = h*gamma, t = max|u|, code = e4m3(u*(448/t)), scale = t*q/448
+//     8 bits: u = h*gamma, t = max|u|, code = nearest(u*(M/t)), scale = t*q/M,
+//     M = 448 (e4m3) or 127 (integers)
 //
 // t does not depend on q, so the sum of squares and the maximum are one
 // reduction: a row costs one exchange between its threads.  TPR threads hold a
@@ -18,107 +19,27 @@
 // The arithmetic is in 64 bits: the kernel is bound by memory, a 64-bit multiply
 // issues at the rate of a 32-bit one here, rows whose squares leave fp32's range
 // stay right (h itself is an fp32 sum, but for the one form below), and a code is
-// the nearest e4m3 value to u*(448/t) itself, not to an fp32 neighbour of it.
+// the nearest value to u*(M/t) itself, not to an fp32 neighbour of it.
 //
 // Measured: 16384 rows of 4096 bf16 channels with residual and sum to e4m3 86 us,
 // 5.4 TB/s, the rate of a copy of that size; 96 rows of 8192 fp16 channels 4.2 us
 // and one row of 4096 2.7 us, latency; 2048 rows of 20480 fp32 channels 135 us, 5.0
 // TB/s, 512 rows 39 us, 4.3 TB/s; 1024 rows of 16384 bf16 channels 32 us, 4.2 TB/s.
+#include <type_traits>
+
 #include "cvx_internal.h"
-#include "tokens.h"
+#include "rows.h"
 
 namespace cvx {
 
 namespace {
 
-typedef _Float16 half_t;
-typedef __bf16 bf16_t;
-
-constexpr float kE4m3Max = 448.0f;
-
-template <typename T, int N>
-struct Vec {
-    typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
-};
-typedef unsigned u32x2 __attribute__((ext_vector_type(2), aligned(1)));
-typedef unsigned u32x1 __attribute__((aligned(1)));
-
-__device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d)
-{
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
-}
-
-// e4m3 takes fp32 values; a 64-bit value goes there rounded to odd (its last bit
-// set if anything is cut), which the rounding to four bits sees as it is.
-__device__ __forceinline__ float to_odd(double v)
-{
-    unsigned long long b = __builtin_bit_cast(unsigned long long, v);
-    const unsigned lo = (unsigned)b;
-    const unsigned cut = (lo & 0xe0000000u) | ((lo & 0x1fffffffu) ? 0x20000000u : 0u);
-    b = (b & 0xffffffff00000000ull) | cut;
-    return (float)__builtin_bit_cast(double, b);
-}
-
-// The value of another lane of the same 16 (a DPP control), or of lane L.
-template <int CTRL>
-__device__ __forceinline__ double lane_move(double v)
-{
-    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
-    const unsigned lo = __builtin_amdgcn_mov_dpp((int)b, CTRL, 0xf, 0xf, true);
-    const unsigned hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xf, 0xf, true);
-    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
-}
-template <int L>
-__device__ __forceinline__ double lane_value(double v)
-{
-    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
-    const unsigned lo = __builtin_amdgcn_readlane((int)b, L), hi = __builtin_amdgcn_readlane((int)(b >> 32), L);
-    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
-}
-// op over the 64 lanes of a wave, whole: within 16 lanes by DPP (neighbour, pair,
-// mirrored half, mirrored row: lanes that hold the same value are interchangeable),
-// then the four rows.  A quarter of the latency of six shuffles by way of LDS.
-template <typename OP>
-__device__ __forceinline__ double wave_all(double v, OP op)
-{
-    v = op(v, lane_move<0xb1>(v));
-    v = op(v, lane_move<0x4e>(v));
-    v = op(v, lane_move<0x141>(v));
-    v = op(v, lane_move<0x140>(v));
-    return op(op(lane_value<0>(v), lane_value<16>(v)), op(lane_value<32>(v), lane_value<48>(v)));
-}
-
-// Row sums over TPR threads of `s` and maxima of `m`; every thread gets both.
-template <int TPR, bool MAX>
-__device__ __forceinline__ void row_reduce(double& s, double& m)
-{
-    s = wave_all(s, [](double a, double b) { return a + b; });
-    if (MAX) m = wave_all(m, [](double a, double b) { return fmax(a, b); });
-    if constexpr (TPR > 64) {
-        constexpr int W = TPR / 64;
-        __shared__ double ls[W];
-        __shared__ double lm[W];
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
-            ls[wave] = s;
-            if (MAX) lm[wave] = m;
-        }
-        __syncthreads();
-        s = 0.0;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            s += ls[i];
-            if (MAX) m = fmax(m, lm[i]);
-        }
-    }
-}
-
-template <typename T, int TPR, int NV, bool RES, bool OUT8>
+template <typename T, int TPR, int NV, bool RES, int OUT>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_rmsnorm(RmsArgs a)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
     constexpr int HOLD = NV > 0 ? NV : 1;
+    constexpr bool OUT8 = OUT != kX16;
     // The sum of two fp32 values can take more than fp32: for codes, which are rounded
     // from h itself, both are held, and h is in 64 bits; else, and of two 16-bit
     // values, their fp32 sum is h, once for the norm and for `sum`.
@@ -239,9 +160,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_rmsnorm(RmsArgs a)
 
     double f = q;
     if constexpr (OUT8) {
-        f = top > 0.0 ? (double)kE4m3Max / top : 0.0;
+        f = top > 0.0 ? kTop<OUT> / top : 0.0;
         // an infinity's row (q = 0) has a NaN scale, also where gamma hides it from `top`
-        if (lane == 0) a.y_scale[row] = q > 0.0 ? (float)(top * q / (double)kE4m3Max) : __builtin_nanf("");
+        if (lane == 0) a.y_scale[row] = q > 0.0 ? (float)(top * q / kTop<OUT>) : __builtin_nanf("");
     }
     each([&](int v, int j) {
         const int i0 = v * VEC;
@@ -253,25 +174,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_rmsnorm(RmsArgs a)
             load_gamma(v, g);
         if constexpr (OUT8) {
             unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.ys;
+            unsigned u[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = to_odd(value(h[j][e], h2[TWO ? j : 0][e]) * (double)g[e] * f);
+            for (int e = 0; e < VEC; ++e) u[e] = code_part<OUT>(value(h[j][e], h2[TWO ? j : 0][e]) * (double)g[e] * f);
             unsigned w[VEC / 4];
 #pragma unroll
-            for (int p = 0; p < VEC / 4; ++p) w[p] = pack_e4m3(o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
-            if (i0 + VEC <= c) {
-                if constexpr (VEC == 8) {
-                    u32x2 w2;
-                    w2[0] = w[0];
-                    w2[1] = w[1];
-                    *reinterpret_cast<u32x2*>(y + i0) = w2;
-                } else {
-                    *reinterpret_cast<u32x1*>(y + i0) = w[0];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (i0 + e < c) y[i0 + e] = (unsigned char)(w[e / 4] >> (8 * (e % 4)));
-            }
+            for (int p = 0; p < VEC / 4; ++p) w[p] = pack_codes<OUT>(u[4 * p], u[4 * p + 1], u[4 * p + 2], u[4 * p + 3]);
+            store_codes<VEC>(y, i0, c, w);
         } else {
             T* y = static_cast<T*>(a.y) + row * a.ys;
 #pragma unroll
@@ -291,17 +200,19 @@ void launch_one(const RmsArgs& a, hipStream_t s)
 {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     const dim3 grid((unsigned)(((long)a.rows + RPB - 1) / RPB)), block(TPR < 256 ? 256 : TPR);
-    if (a.res) {
-        if (a.out8)
-            hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, true, true>), grid, block, 0, s, a);
+    auto go = [&](auto res) {
+        constexpr bool RES = decltype(res)::value;
+        if (a.held == kX16)
+            hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, RES, kX16>), grid, block, 0, s, a);
+        else if (a.held == kXE4m3)
+            hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, RES, kXE4m3>), grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, true, false>), grid, block, 0, s, a);
-    } else {
-        if (a.out8)
-            hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, false, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, false, false>), grid, block, 0, s, a);
-    }
+            hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, RES, kXI8>), grid, block, 0, s, a);
+    };
+    if (a.res)
+        go(std::true_type());
+    else
+        go(std::false_type());
 }
 
 template <typename T>
@@ -345,7 +256,7 @@ hipError_t launch_rmsnorm(const RmsArgs& all, int dtype, hipStream_t s)
 {
     // at most 2^20 rows a launch: a grid holds fewer than 2^32 threads
     constexpr int kRows = 1 << 20;
-    const long es = dtype == CVX_DT_F32 ? 4 : 2, eo = all.out8 ? 1 : es;
+    const long es = dtype == CVX_DT_F32 ? 4 : 2, eo = all.held != kX16 ? 1 : es;
     for (long r0 = 0; r0 < all.rows; r0 += kRows) {
         RmsArgs a = all;
         a.rows = all.rows - r0 < kRows ? (int)(all.rows - r0) : kRows;
@@ -353,7 +264,7 @@ hipError_t launch_rmsnorm(const RmsArgs& all, int dtype, hipStream_t s)
         if (all.res) a.res = static_cast<const char*>(all.res) + r0 * all.rs * es;
         if (all.sum) a.sum = static_cast<char*>(all.sum) + r0 * all.ss * es;
         a.y = static_cast<char*>(all.y) + r0 * all.ys * eo;
-        if (all.out8) a.y_scale = all.y_scale + r0;
+        if (all.held != kX16) a.y_scale = all.y_scale + r0;
         const hipError_t e = dtype == CVX_DT_F32   ? launch_t<float>(a, s)
                              : dtype == CVX_DT_F16 ? launch_t<half_t>(a, s)
                                                    : launch_t<bf16_t>(a, s);

@@ -18,7 +18,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef half_t h8 __attribute__((ext_vector_type(8)));
 typedef half_t h4 __attribute__((ext_vector_type(4)));
 typedef bf16_t b8 __attribute__((ext_vector_type(8)));
@@ -61,11 +63,27 @@ __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c)
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
 }
 
-// eight e4m3 values -> eight 16-bit values, exactly
-template <typename T>
+// The same blocks of 8-bit integers, exactly: sixteen values of k a lane, from
+// 16*(l/16) of 64 and from 16*(l/32) of 32.
+__device__ __forceinline__ i32x4 mma16_i8(u32x4 a, u32x4 b, i32x4 c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ i32x16 mma32_i8(u32x4 a, u32x4 b, i32x16 c)
+{
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// eight e4m3 values or 8-bit integers -> eight 16-bit values, exactly
+template <typename T, int X>
 __device__ __forceinline__ u32x4 widen8(u32x2 q)
 {
     typename V16<T>::v8 o;
+    if constexpr (X == kXI8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = (T)(float)(signed char)(q[i / 4] >> (8 * (i % 4)));
+        return __builtin_bit_cast(u32x4, o);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
@@ -76,6 +94,22 @@ __device__ __forceinline__ u32x4 widen8(u32x2 q)
         o[4 * i + 3] = (T)hi[1];
     }
     return __builtin_bit_cast(u32x4, o);
+}
+
+// f(type of the output, what x and w are held in), both as values that carry them.
+template <typename T>
+struct TypeOf {
+    typedef T type;
+};
+template <typename F>
+hipError_t by_types(int dtype, int held, F f)
+{
+    auto of = [&](auto t) {
+        return held == kX16     ? f(t, std::integral_constant<int, kX16>())
+               : held == kXE4m3 ? f(t, std::integral_constant<int, kXE4m3>())
+                                : f(t, std::integral_constant<int, kXI8>());
+    };
+    return dtype == CVX_DT_F16 ? of(TypeOf<half_t>()) : of(TypeOf<bf16_t>());
 }
 
 typedef __attribute__((address_space(3))) void lds_void;

@@ -1,0 +1,272 @@
+// lin_tile.h -- the products of a tile of output channels x tokens on the matrix
+// cores, which the projection of many tokens and the products grouped by expert share.
+//
+// A stage is 128 bytes of every row of both operands, loaded straight into LDS; the
+// 16-byte pieces of a row are permuted by the row's index as they are fetched, so that
+// the lanes of an operand read (32 rows, the same piece) fall in different banks while
+// every fetch still takes whole 128-byte lines.  Stage s+1 (and, with four stage
+// buffers, up to s+3) arrives while s is multiplied; a stage has one barrier, before
+// which a wave waits for its own fetches of the next stage only, and which drains
+// nothing.
+#pragma once
+
+#include "lin_common.h"
+
+namespace cvx {
+
+// Orders this wave's LDS accesses (which the hardware keeps in order) for the compiler.
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The operands of a tile: rows of `cb` bytes; lane's byte offsets of its fetches
+// (eight rows each; a row that is not there at kOOB or past the range) from bases that
+// move with the stage, and the bytes from a base to its operand's end.
+struct TileRows {
+    const char *w, *x;
+    unsigned wend, xend;
+    unsigned wo[8], xo[8];
+};
+
+// T: 16-bit type; X: what the operands are held in (kX16: T).  WM x WN waves, each
+// MB x NB blocks of 32 x 32; D stage buffers.
+template <typename T, int X, int WM, int WN, int MB, int NB, int D>
+struct Tile {
+    static constexpr bool X8 = X == kXE4m3;
+    static constexpr bool I8 = X == kXI8;
+    static constexpr unsigned XB = X == kX16 ? 2 : 1;  // bytes of an operand's value
+    static constexpr int W = WM * WN, NT = 64 * W;
+    static constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
+    static constexpr int FM = BM / (8 * W), FN = BN / (8 * W);  // fetches of eight rows a wave, per stage and operand
+    static constexpr int STEPS = X8 ? 2 : 4;
+    static constexpr int SB = (BM + BN) * 128;  // bytes of a stage
+    static_assert(D == 2 || D == 4, "stage buffers");
+    static_assert(W * 4096 <= SB && MB % 2 == 0, "LDS is used again after the main loop");
+    static_assert(W % 2 == 0, "a wave's fetches begin at rows 8 * wave + 16 * i");
+    static_assert(FM <= 8 && FN <= 8, "fetches a wave");
+    typedef typename V16<T>::v4 v4;
+    typedef typename std::conditional<X8, i32x8, u32x4>::type op_t;
+    // sums: of 8-bit integers exact ones
+    typedef typename std::conditional<I8, i32x16, f32x16>::type sum_t;
+
+    // The 16-byte piece this lane fetches of its row of a fetch: the pieces of row r lie
+    // permuted, piece p at p ^ (r/2 % 8); the sixteen lanes of an operand read that go
+    // together (0-3, 12-15, 20-27 of 32, or the others) then fall in all of the banks.
+    static __device__ __forceinline__ unsigned piece(int wave, int lane)
+    {
+        return (unsigned)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
+    }
+    // The row of the tile that this lane's part of fetch i is of.
+    static __device__ __forceinline__ int fetch_row(int wave, int lane, int i) { return 8 * (wave + W * i) + (lane >> 3); }
+
+    // The sums over all stages of rows of cb bytes.  All waves of the workgroup call
+    // it; nothing is under way in LDS before, and nothing after.
+    static __device__ __forceinline__ void sums(const TileRows& o, unsigned cb, int wave, int lane, unsigned char* buf0,
+                                                unsigned char* buf1, unsigned char* buf2, unsigned char* buf3,
+                                                sum_t (&acc)[MB][NB])
+    {
+        const int wm = wave % WM, wn = wave / WM;
+        const int hi = lane >> 5, l32 = lane & 31;
+        const int nst = (int)((cb + 127) / 128);
+        const unsigned pc = piece(wave, lane);
+        auto issue = [&](int st, unsigned char* buf) {
+            const unsigned kb = (unsigned)st * 128 < cb ? (unsigned)st * 128 : 0u;  // past the end: nothing is live
+            const unsigned dead = (unsigned)st * 128 + pc < cb ? 0u : kOOB;
+            const char *wk = o.w + kb, *xk = o.x + kb;
+            const unsigned wleft = o.wend - kb, xleft = o.xend - kb;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wk, wleft), (lds_void*)(buf + 1024 * (wave + W * i)), 16,
+                                                         o.wo[i] | dead, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xk, xleft),
+                                                         (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16,
+                                                         o.xo[i] | dead, 0, 0, 0);
+        };
+        unsigned slot[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) slot[s] = (unsigned)(l32 * 128 + (((2 * s + hi) ^ ((l32 >> 1) & 7)) * 16));
+        auto read = [&](const unsigned char* buf, int st, op_t(&A)[MB], op_t(&B)[NB]) {
+            const unsigned char* pa = buf + wm * MB * 4096;
+            const unsigned char* pb = buf + BM * 128 + wn * NB * 4096;
+            auto one = [&](const unsigned char* p) {
+                if constexpr (X8) {
+                    const u32x4 x = *reinterpret_cast<const u32x4*>(p + slot[2 * st]);
+                    const u32x4 y = *reinterpret_cast<const u32x4*>(p + slot[2 * st + 1]);
+                    i32x8 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = (int)x[e];
+                        v[4 + e] = (int)y[e];
+                    }
+                    return v;
+                } else {
+                    return *reinterpret_cast<const u32x4*>(p + slot[st]);
+                }
+            };
+#pragma unroll
+            for (int n = 0; n < NB; ++n) B[n] = one(pb + 4096 * n);
+#pragma unroll
+            for (int m = 0; m < MB; ++m) A[m] = one(pa + 4096 * m);
+        };
+
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[m][n][e] = 0;
+        auto mul = [&](const op_t(&A)[MB], const op_t(&B)[NB]) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    if constexpr (X8)
+                        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A[m], B[n], acc[m][n], 0, 0, 0,
+                                                                                    0x7f7f7f7f, 0, 0x7f7f7f7f);
+                    else if constexpr (I8)
+                        acc[m][n] = mma32_i8(A[m], B[n], acc[m][n]);
+                    else
+                        acc[m][n] = mma32<T>(A[m], B[n], acc[m][n]);
+                }
+        };
+        // Orders a step's instructions: the reads of the next operands and the fetches
+        // of a later stage between the matrix instructions.
+        auto mix = [&](auto fetches) {
+            constexpr int READS = (X8 ? 2 : 1) * (MB + NB), MUL = MB * NB, F = decltype(fetches)::value;
+            constexpr int OTHER = READS + F;
+#pragma unroll
+            for (int i = 0; i < MUL; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+#pragma unroll
+                for (int q = i * OTHER / MUL; q < (i + 1) * OTHER / MUL; ++q) {
+                    if (q < READS)
+                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    else
+                        __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+                }
+            }
+        };
+        auto mix_all = [&]() {  // the same for a whole stage
+            constexpr int READS = (X8 ? 2 : 1) * (MB + NB) * STEPS, MUL = MB * NB * STEPS, OTHER = READS + FM + FN;
+#pragma unroll
+            for (int i = 0; i < MUL; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+#pragma unroll
+                for (int q = i * OTHER / MUL; q < (i + 1) * OTHER / MUL; ++q) {
+                    if (q % (OTHER / (FM + FN)) == 0)
+                        __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+                    else
+                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+            }
+        };
+        // Both loops take D stages; those past the last are zeros, and so are the fetches past it.
+        typedef std::integral_constant<int, FM + FN> fetch;
+        if constexpr (D == 2) {
+            // A step's operands are read under the step before.
+            typedef std::integral_constant<int, 0> no_fetch;
+            op_t A0[MB], B0[NB], A1[MB], B1[NB];
+            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
+#pragma unroll
+                for (int s = 0; s + 1 < STEPS; ++s) {
+                    if (s & 1) {
+                        read(cur, s + 1, A0, B0);
+                        mul(A1, B1);
+                    } else {
+                        read(cur, s + 1, A1, B1);
+                        mul(A0, B0);
+                    }
+                    mix(no_fetch());
+                }
+                wait_arrived<0>();  // the next stage has arrived, this wave has read the current one
+                stage_barrier();
+                issue(st + 2, cur);
+                read(nxt, 0, A0, B0);
+                mul(A1, B1);
+                mix(fetch());
+            };
+            issue(0, buf0);
+            wait_arrived<0>();
+            stage_barrier();
+            issue(1, buf1);
+            read(buf0, 0, A0, B0);
+            for (int st = 0; st < nst; st += 2) {
+                stage(st, buf0, buf1);
+                stage(st + 1, buf1, buf0);
+            }
+        } else {
+            // One wave a SIMD: a stage's operands are all read under the stage before, as
+            // a step's products (four instructions) are shorter than a read takes.
+            op_t A0[STEPS][MB], B0[STEPS][NB], A1[STEPS][MB], B1[STEPS][NB];
+            auto read_all = [&](const unsigned char* buf, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB]) {
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) read(buf, s, A[s], B[s]);
+            };
+            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB],
+                             op_t(&An)[STEPS][MB], op_t(&Bn)[STEPS][NB]) {
+                wait_arrived<2 * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
+                stage_barrier();
+                issue(st + 4, cur);
+                read_all(nxt, An, Bn);
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) mul(A[s], B[s]);
+                mix_all();
+            };
+            issue(0, buf0);
+            issue(1, buf1);
+            issue(2, buf2);
+            issue(3, buf3);
+            wait_arrived<3 * (FM + FN)>();
+            stage_barrier();
+            read_all(buf0, A0, B0);
+            for (int st = 0; st < nst; st += 4) {
+                stage(st, buf0, buf1, A0, B0, A1, B1);
+                stage(st + 1, buf1, buf2, A1, B1, A0, B0);
+                stage(st + 2, buf2, buf3, A0, B0, A1, B1);
+                stage(st + 3, buf3, buf0, A1, B1, A0, B0);
+            }
+        }
+        wait_arrived<0>();  // no fetch is under way when LDS is used again
+        stage_barrier();
+    }
+
+    // Writes finished values, `out`[n][m] a lane's sixteen channels of a token, four at a
+    // time: they are turned in LDS (4 KB a wave from `room`), so that a store takes whole
+    // lines.  ry: the rows from the tile's first token; m0: its first channel.
+    static __device__ __forceinline__ void store(const v4 (&out)[NB][MB][4], unsigned char* room, int wave, int lane,
+                                                 rsrc_t ry, int nrows, unsigned ys, int m0, int cout)
+    {
+        const int wm = wave % WM, wn = wave / WM;
+        const int hi = lane >> 5, l32 = lane & 31;
+        unsigned char* turn = room + wave * 4096;
+        const int p = lane & 7;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < MB; m += 2) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<v4*>(turn + l32 * 128 + ((k ^ (l32 & 7)) * 16) + 8 * hi) = out[n][m + k / 4][k % 4];
+                wave_lds_order();
+                const int c = m0 + (wm * MB + m) * 32 + 8 * p;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tt = 8 * i + (lane >> 3), t = (wn * NB + n) * 32 + tt;
+                    const u32x4 q = *reinterpret_cast<const u32x4*>(turn + tt * 128 + ((p ^ (tt & 7)) * 16));
+                    const unsigned off = ((unsigned)t * ys + (unsigned)c) * 2u;
+                    const bool live = t < nrows;
+                    __builtin_amdgcn_raw_buffer_store_b128(q, ry, live && c + 8 <= cout ? (int)off : (int)kOOB, 0, 0);
+                    if (cout & 4)  // the last four channels of a row
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{q[0], q[1]}, ry,
+                                                              live && c + 4 == cout ? (int)off : (int)kOOB, 0, 0);
+                }
+                wave_lds_order();
+            }
+    }
+};
+
+}  // namespace cvx

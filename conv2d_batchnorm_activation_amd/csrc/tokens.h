@@ -11,6 +11,14 @@
 
 namespace cvx {
 
+// What a projection's x and w, or the rows made for one, are held in, as a kernel's
+// parameter: the other operands' type, e4m3, 8-bit integers.
+constexpr int kX16 = 0, kXE4m3 = 1, kXI8 = 2;
+inline int held_of(int dtype, int x_dtype)
+{
+    return x_dtype == dtype ? kX16 : x_dtype == CVX_DT_E4M3 ? kXE4m3 : kXI8;
+}
+
 // ------------------------------------------------------------------ the norm
 struct RmsArgs {
     const void* x;
@@ -22,7 +30,7 @@ struct RmsArgs {
     long xs, rs, ss, ys;  // row strides, elements
     int rows, c;
     float eps;
-    int out8;
+    int held;             // y: kX16 for dtype (32 bits too), or an 8-bit type
 };
 hipError_t launch_rmsnorm(const RmsArgs& a, int dtype, hipStream_t s);
 
@@ -74,9 +82,9 @@ inline size_t lora_joined_bytes(long tokens, int rank) { return (size_t)(rank + 
 
 LinPlan linear_plan(const cvx_linear_desc& d);
 void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int len);
-hipError_t launch_lora_down(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s);
+hipError_t launch_lora_down(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s);
 hipError_t launch_lora_join(const LinArgs& a, int dtype, hipStream_t s);
-hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s);
-hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int x8, hipStream_t s);
+hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s);
+hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s);
 
 }  // namespace cvx

@@ -31,7 +31,7 @@ CVX_RES_NONE, CVX_RES_BEFORE_ACT, CVX_RES_AFTER_ACT = 0, 1, 2
 CVX_L_CONV, CVX_L_GAP, CVX_L_FC, CVX_L_PREPROC = 0, 1, 2, 3
 CVX_INPUT, CVX_NO_RES = -1, -2
 CVX_W_OIHW, CVX_W_PACKED = 0, 1
-CVX_DT_F32, CVX_DT_F16, CVX_DT_BF16, CVX_DT_E4M3 = 0, 1, 2, 3
+CVX_DT_F32, CVX_DT_F16, CVX_DT_BF16, CVX_DT_E4M3, CVX_DT_I8 = 0, 1, 2, 3, 4
 STATUS_NAMES = {0: "CVX_OK", -1: "CVX_ERR_NULL", -2: "CVX_ERR_SHAPE", -3: "CVX_ERR_UNSUPPORTED",
                 -4: "CVX_ERR_ALIGN", -5: "CVX_ERR_ALIAS", -6: "CVX_ERR_WORKSPACE",
                 -7: "CVX_ERR_HIP", -8: "CVX_ERR_ARG", -9: "CVX_ERR_SCRATCH"}
@@ -326,7 +326,7 @@ def make_rmsnorm_desc(rows, c, dtype, out_dtype=None, eps=1e-6, x_stride=0, res_
 #: what an operand on tokens is held in, by its type in the descriptor; a type that is none of
 #: these is the library's to refuse
 _HELD = {CVX_DT_F32: torch.float32, CVX_DT_F16: torch.float16, CVX_DT_BF16: torch.bfloat16,
-         CVX_DT_E4M3: torch.float8_e4m3fn}
+         CVX_DT_E4M3: torch.float8_e4m3fn, CVX_DT_I8: torch.int8}
 _F32, _I32 = torch.float32, torch.int32
 
 

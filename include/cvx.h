@@ -347,14 +347,15 @@ CVX_API cvx_status cvx_conv_bn_act_nhwc(const cvx_conv_desc *d, int dtype, const
  * is an operand as it is.  Where two operands must not overlap, what counts is
  * the range from an operand's first byte to its last. */
 
-/* Element type of 8-bit values: e4m3 (4 exponent bits, 3 fraction bits, largest
- * value 448, no infinities).  Only the operators of this section take it. */
-enum { CVX_DT_E4M3 = 3 };
+/* Element types of 8-bit values: e4m3 (4 exponent bits, 3 fraction bits, largest
+ * value 448, no infinities) and signed integers.  Only the operators of this
+ * section take them. */
+enum { CVX_DT_E4M3 = 3, CVX_DT_I8 = 4 };
 
 typedef struct cvx_rmsnorm_desc {
     int rows, c;        /* x [rows][c]; both at least 1, c at most 2^30          */
     int dtype;          /* CVX_DT_F32, _F16 or _BF16: x, residual, sum           */
-    int out_dtype;      /* type of y: dtype, or CVX_DT_E4M3                      */
+    int out_dtype;      /* type of y: dtype, CVX_DT_E4M3 or CVX_DT_I8            */
     float eps;          /* > 0, finite                                           */
     long x_stride, res_stride, sum_stride, y_stride; /* row strides, 0 or >= c  */
 } cvx_rmsnorm_desc;
@@ -369,11 +370,12 @@ typedef struct cvx_rmsnorm_desc {
  * infinity where that overflows; squares, sums and products are taken in 64 bits, so
  * no row whose h is finite overflows them.  One form is wider: of fp32 rows with a
  * residual and 8-bit output h enters the norm in 64 bits, so that a code is the
- * nearest to its value, and only `sum` can overflow.  With out_dtype = CVX_DT_E4M3,
- * u_i = h_i*gamma_i and t = max_i |u_i|,
- *     y_i = e4m3(u_i * (448/t)),  y_scale = t*q/448     (t = 0: zeros)
- * so that y_i * y_scale is the norm's output; q, which depends on the whole
- * row's sum, cancels in the codes.
+ * nearest to its value, and only `sum` can overflow.  With 8-bit output,
+ * u_i = h_i*gamma_i, t = max_i |u_i| and M = 448 (e4m3) or 127 (integers),
+ *     y_i = code(u_i * (M/t)),  y_scale = t*q/M         (t = 0: zeros)
+ * the nearest e4m3 value or integer (ties to even; -128 is never one), so that
+ * y_i * y_scale is the norm's output; q, which depends on the whole row's sum,
+ * cancels in the codes.
  * A row that holds a NaN gives NaN throughout (8 bits: a NaN scale); one that
  * holds an infinity gives NaN in its place and zeros elsewhere (8 bits: a NaN
  * scale); other rows are not touched by it.
@@ -382,7 +384,7 @@ typedef struct cvx_rmsnorm_desc {
  *   sum         : device [rows][c] of dtype, or NULL when h is not wanted.  May be the
  *                 same tensor as x or as residual (same address and stride).
  *   y           : device [rows][c] of out_dtype, aligned to an element.
- *   y_scale     : device fp32 [rows]; required iff out_dtype is CVX_DT_E4M3.
+ *   y_scale     : device fp32 [rows]; required iff out_dtype is an 8-bit type.
  * y, y_scale and sum must not overlap one another or, but for sum as said, an input.
  * Rows aligned to 16 bytes are fastest; others give the same results.
  * Errors: CVX_ERR_NULL, CVX_ERR_SHAPE (rows or c < 1, c > 2^30, a stride between 0
@@ -397,7 +399,7 @@ typedef struct cvx_linear_desc {
     int c_in, c_out;    /* channels, at most 2^20 each; tokens * c_out at most 2^37,
                          * and no operand more than 2^40 elements from first to last  */
     int dtype;          /* CVX_DT_F16 or _BF16: y, residual, adapters             */
-    int x_dtype;        /* type of x and w: dtype, or CVX_DT_E4M3                 */
+    int x_dtype;        /* type of x and w: dtype, CVX_DT_E4M3 or CVX_DT_I8       */
     int act;            /* CVX_ACT_*                                              */
     int res_mode;       /* CVX_RES_*                                              */
     int rank;           /* rank of the adapters, 0 = no adapters                  */
@@ -419,7 +421,8 @@ CVX_API cvx_status cvx_linear_plan(const cvx_linear_desc *d, char *buf, int buf_
  *     z_t[o]   = scale[o] * x_scale[t] * sum_i w[o][i]*x[t][i] + bias[o]
  *                + lora_alpha[d] * sum_r lora_b[d][o][r] * v_t[r]
  *     y        = act(z [+ residual]) [+ residual]                      by d->res_mode
- * Products are accumulated in fp32 (with 8-bit operands and more than 64 tokens,
+ * Sums of 8-bit integers (-128 among them) are exact 32-bit integers, rounded to fp32
+ * once; others are accumulated in fp32 (with e4m3 operands and more than 64 tokens,
  * the matrix cores align the products of eight consecutive channels to the
  * largest of them and drop what lies 2^-13 below it: about 2^-16 of the result's
  * size on normal values, 2^-14 with one channel in 64 a hundred times larger; who
@@ -431,7 +434,7 @@ CVX_API cvx_status cvx_linear_plan(const cvx_linear_desc *d, char *buf, int buf_
  * every activation (max(0, NaN) is NaN here, where the convolutions give 0).  Results
  * do not depend on timing.
  *   x          : device [tokens][c_in] of x_dtype, 16-byte aligned rows.
- *   x_scale    : device fp32 [tokens]; required iff x_dtype is CVX_DT_E4M3
+ *   x_scale    : device fp32 [tokens]; required iff x_dtype is an 8-bit type
  *                (cvx_rmsnorm's y and y_scale are such operands).
  *   w          : device [c_out][c_in] of x_dtype, dense, 16-byte aligned.
  *   scale, bias: device fp32 [c_out], 16-byte aligned; NULL means 1 and 0.  8-bit
@@ -449,9 +452,9 @@ CVX_API cvx_status cvx_linear_plan(const cvx_linear_desc *d, char *buf, int buf_
  * multiple of 8 up to 128 (adapters of lower rank are padded with zero rows and
  * columns), x_stride a multiple of 8 (16 in 8 bits), y_stride and res_stride
  * multiples of 4; else CVX_ERR_UNSUPPORTED.
- * Errors otherwise: CVX_ERR_NULL, CVX_ERR_SHAPE, CVX_ERR_ARG (types, act,
- * res_mode, a rank without adapters or adapters without a rank), CVX_ERR_ALIGN,
- * CVX_ERR_ALIAS, CVX_ERR_WORKSPACE, CVX_ERR_HIP.
+ * Errors otherwise: CVX_ERR_NULL, CVX_ERR_SHAPE (sizes, strides, more than 2^17 - 16
+ * channels in of 8-bit integers), CVX_ERR_ARG (types, act, res_mode, a rank without
+ * adapters or adapters without a rank), CVX_ERR_ALIGN, CVX_ERR_ALIAS, CVX_ERR_WORKSPACE, CVX_ERR_HIP.
  */
 CVX_API cvx_status cvx_linear(const cvx_linear_desc *d, const void *x, const float *x_scale, const void *w,
                               const float *scale, const float *bias, const void *residual,
