@@ -121,6 +121,41 @@ cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc* d, const void* x, const void* res
     return launch_rmsnorm(a, d->dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? CVX_OK : CVX_ERR_HIP;
 }
 
+cvx_status cvx_gate(const cvx_gate_desc* d, const void* gate, const void* up, void* y, float* y_scale, void* stream)
+{
+    if (d == nullptr) return CVX_ERR_NULL;
+    if (d->dtype != CVX_DT_F32 && !dtype16(d->dtype)) return CVX_ERR_ARG;
+    if (d->out_dtype != d->dtype && !dtype8(d->out_dtype)) return CVX_ERR_ARG;
+    if (d->act < CVX_ACT_NONE || d->act > CVX_ACT_SILU) return CVX_ERR_ARG;
+    if (d->rows < 1 || d->c < 1 || d->c > kMaxNormed) return CVX_ERR_SHAPE;
+    const bool out8 = dtype8(d->out_dtype);
+    GateArgs a;
+    a.us = d->c;
+    if (!stride_of(d->gate_stride, d->c, d->rows, &a.gs) || !stride_of(d->y_stride, d->c, d->rows, &a.ys) ||
+        (up && !stride_of(d->up_stride, d->c, d->rows, &a.us)))
+        return CVX_ERR_SHAPE;
+    if (!gate || !y || (out8 && !y_scale)) return CVX_ERR_NULL;
+    const unsigned es = dt_bytes(d->dtype), eo = dt_bytes(d->out_dtype);
+    if (!aligned_to(gate, es) || !aligned_to(up, es) || !aligned_to(y, eo) || (out8 && !aligned_to(y_scale, 4)))
+        return CVX_ERR_ALIGN;
+    const Span in[2] = {rows_span(gate, d->rows, a.gs, d->c, es),
+                        up ? rows_span(up, d->rows, a.us, d->c, es) : Span{0, 0}};
+    const Span out[2] = {rows_span(y, d->rows, a.ys, d->c, eo), out8 ? bytes_span(y_scale, 4ul * d->rows) : Span{0, 0}};
+    if (meets(out[0], out[1])) return CVX_ERR_ALIAS;
+    for (const Span& o : out)
+        for (const Span& i : in)
+            if (meets(o, i)) return CVX_ERR_ALIAS;
+    a.gate = gate;
+    a.up = up;
+    a.y = y;
+    a.y_scale = y_scale;
+    a.rows = d->rows;
+    a.c = d->c;
+    a.act = d->act;
+    a.held = held_of(d->dtype, d->out_dtype);
+    return launch_gate(a, d->dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? CVX_OK : CVX_ERR_HIP;
+}
+
 size_t cvx_linear_workspace_bytes(const cvx_linear_desc* d)
 {
     long xs, rs, ys;

@@ -1,0 +1,269 @@
+// k_gate.hip -- the gated activation between two projections, and rows of any
+// origin brought to 8 bits:
+//
+//     u = act(g) * up   (act(g) alone without `up`),   y = u rounded
+//     8 bits: t = max|u|, code = nearest(u*(M*(1/t))), scale = t/M, M = 448 or 127
+//
+// Bound by memory: every value is read once and written once.  With 8-bit output a
+// row's largest magnitude is one reduction between the TPR threads that hold it, as NV
+// 16-byte vectors an operand each; rows too long to be held (NV = 0) are read a second
+// time.  u is then taken and held in 64 bits, so that a code is the nearest to its
+// value and integers do not depend on how the exponential was rounded: some 35 64-bit
+// instructions a value, issued at the rate of 32-bit ones.  Otherwise u is in fp32
+// and there is no row: a thread takes a vector.
+#include <type_traits>
+
+#include "cvx_internal.h"
+#include "rows.h"
+
+namespace cvx {
+
+namespace {
+
+// exp(x), x clamped to where the result is 0, finite or infinite: 2^n * e^r with
+// |r| <= ln(2)/2 and the series of e^r to r^12, which leaves 2e-16 of it.
+__device__ __forceinline__ double exp64(double x)
+{
+    x = fmin(fmax(x, -1100.0), 1100.0);
+    const double n = rint(x * 1.4426950408889634);
+    double r = fma(-n, 0x1.62e42fefa39efp-1, x);  // ln(2) to 53 bits, and what is left of it
+    r = fma(-n, 0x1.abc9e3b39803fp-56, r);
+    double p = 1.0 / 479001600.0;
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
+}
+
+template <int ACT>
+__device__ __forceinline__ double act64(double g)
+{
+    if constexpr (ACT == CVX_ACT_RELU) return g < 0.0 ? 0.0 : g;  // a NaN stays one
+    if constexpr (ACT == CVX_ACT_SILU) {
+        const double d = 1.0 + exp64(-g);
+        double q = __builtin_amdgcn_rcp(d);  // good to 2^-26 or so: two steps double that twice
+        q = fma(fma(-d, q, 1.0), q, q);
+        q = fma(fma(-d, q, 1.0), q, q);
+        return g * (d < 1.0e300 ? q : 0.0);  // (the steps make a NaN of an infinity)
+    }
+    return g;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act32(float g)
+{
+    if constexpr (ACT == CVX_ACT_RELU) return g < 0.0f ? 0.0f : g;
+    if constexpr (ACT == CVX_ACT_SILU) return g / (1.0f + expf(-g));
+    return g;
+}
+
+// VEC values of an operand from channel i0, zero past c.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, int i0, int c, float (&o)[VEC])
+{
+    typedef typename Vec<T, VEC>::type V;
+    if (i0 + VEC <= c) {
+        const V v = *reinterpret_cast<const V*>(p + i0);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = (float)v[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = i0 + e < c ? (float)p[i0 + e] : 0.0f;
+    }
+}
+
+// 8-bit output: TPR threads a row.
+template <typename T, int TPR, int NV, int ACT, bool UP, int OUT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_gate(GateArgs a)
+{
+    constexpr int VEC = 16 / (int)sizeof(T);
+    constexpr int HOLD = NV > 0 ? NV : 1;
+    const int lane = threadIdx.x % TPR;
+    const long row = TPR < 256 ? (long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR : (long)blockIdx.x;
+    if (row >= a.rows) return;  // whole waves: a row has at least one
+    const T* g = static_cast<const T*>(a.gate) + row * a.gs;
+    const T* p = UP ? static_cast<const T*>(a.up) + row * a.us : nullptr;
+    unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.ys;
+    const int c = a.c, nvec = (c + VEC - 1) / VEC;
+
+    float gv[HOLD][VEC], uv[UP ? HOLD : 1][VEC];
+    auto load = [&](int v, int j) {
+        load_vec<T, VEC>(g, v * VEC, c, gv[j]);
+        if constexpr (UP) load_vec<T, VEC>(p, v * VEC, c, uv[UP ? j : 0]);
+    };
+    auto value = [&](int j, int e) {
+        const double u = act64<ACT>((double)gv[j][e]);
+        return UP ? u * (double)uv[UP ? j : 0][e] : u;
+    };
+    double held[HOLD][VEC], top = 0.0, odd = 0.0;
+    auto look = [&](int j) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            held[j][e] = value(j, e);
+            top = fmax(top, fabs(held[j][e]));
+            odd = fma(held[j][e], 0.0, odd);  // a NaN from the first NaN or infinity on
+        }
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane + j * TPR < nvec) load(lane + j * TPR, j);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane + j * TPR < nvec) look(j);
+    } else {
+        for (int v = lane; v < nvec; v += TPR) {
+            load(v, 0);
+            look(0);
+        }
+    }
+    if (odd != 0.0) top = __builtin_inf();
+    double none = 0.0;
+    row_reduce<TPR, true>(none, top);
+    const bool bad = top > 1.7e308;
+    const double f = top > 0.0 && !bad ? kTop<OUT> * (1.0 / top) : 0.0;
+    if (lane == 0) a.y_scale[row] = bad ? __builtin_nanf("") : (float)(top / kTop<OUT>);
+    auto put = [&](int v, int j) {
+        unsigned u[VEC], w[VEC / 4];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) u[e] = code_part<OUT>(held[j][e] * f);
+#pragma unroll
+        for (int q = 0; q < VEC / 4; ++q) w[q] = pack_codes<OUT>(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+        store_codes<VEC>(y, v * VEC, c, w);
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (lane + j * TPR < nvec) put(lane + j * TPR, j);
+    } else {
+        for (int v = lane; v < nvec; v += TPR) {
+            load(v, 0);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) held[0][e] = value(0, e);
+            put(v, 0);
+        }
+    }
+}
+
+// Output of the inputs' type: a thread a vector.
+template <typename T, int ACT, bool UP>
+__global__ void __launch_bounds__(256) k_gate_wide(GateArgs a)
+{
+    constexpr int VEC = 16 / (int)sizeof(T);
+    typedef typename Vec<T, VEC>::type V;
+    const unsigned nvec = (unsigned)(a.c + VEC - 1) / VEC;
+    const long at = (long)blockIdx.x * 256 + threadIdx.x;
+    const long row = at / nvec;
+    const int i0 = (int)(at - row * nvec) * VEC, c = a.c;
+    if (row >= a.rows) return;
+    float g[VEC], u[VEC];
+    load_vec<T, VEC>(static_cast<const T*>(a.gate) + row * a.gs, i0, c, g);
+    if constexpr (UP) load_vec<T, VEC>(static_cast<const T*>(a.up) + row * a.us, i0, c, u);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        g[e] = act32<ACT>(g[e]);
+        if constexpr (UP) g[e] *= u[e];
+    }
+    T* y = static_cast<T*>(a.y) + row * a.ys;
+    if (i0 + VEC <= c) {
+        V o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = (T)g[e];
+        *reinterpret_cast<V*>(y + i0) = o;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (i0 + e < c) y[i0 + e] = (T)g[e];
+    }
+}
+
+// f(the activation, whether there is an `up`), as values that carry them
+template <typename F>
+void by_act(const GateArgs& a, F f)
+{
+    auto of = [&](auto act) {
+        if (a.up)
+            f(act, std::true_type());
+        else
+            f(act, std::false_type());
+    };
+    if (a.act == CVX_ACT_SILU)
+        of(std::integral_constant<int, CVX_ACT_SILU>());
+    else if (a.act == CVX_ACT_RELU)
+        of(std::integral_constant<int, CVX_ACT_RELU>());
+    else
+        of(std::integral_constant<int, CVX_ACT_NONE>());
+}
+
+template <typename T, int TPR, int NV>
+void launch_rows(const GateArgs& a, hipStream_t s)
+{
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    const dim3 grid((unsigned)(((long)a.rows + RPB - 1) / RPB)), block(TPR < 256 ? 256 : TPR);
+    by_act(a, [&](auto act, auto up) {
+        if (a.held == kXE4m3)
+            hipLaunchKernelGGL((k_gate<T, TPR, NV, act.value, up.value, kXE4m3>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((k_gate<T, TPR, NV, act.value, up.value, kXI8>), grid, block, 0, s, a);
+    });
+}
+
+template <typename T>
+hipError_t launch_t(const GateArgs& a, hipStream_t s)
+{
+    constexpr int VEC = 16 / (int)sizeof(T);
+    const long nvec = ((long)a.c + VEC - 1) / VEC;
+    if (a.held == kX16) {
+        const dim3 grid((unsigned)((a.rows * nvec + 255) / 256));
+        by_act(a, [&](auto act, auto up) {
+            hipLaunchKernelGGL((k_gate_wide<T, act.value, up.value>), grid, dim3(256), 0, s, a);
+        });
+    } else if (nvec <= 64) {
+        launch_rows<T, 64, 1>(a, s);
+    } else if (nvec <= 256) {
+        launch_rows<T, 256, 1>(a, s);
+    } else if (nvec <= 512) {
+        launch_rows<T, 256, 2>(a, s);
+    } else if (nvec <= 1024) {
+        launch_rows<T, 1024, 1>(a, s);
+    } else if (nvec <= 2048) {
+        launch_rows<T, 1024, 2>(a, s);
+    } else {
+        launch_rows<T, 1024, 0>(a, s);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gate(const GateArgs& all, int dtype, hipStream_t s)
+{
+    // as many rows a launch as keep a grid below 2^32 threads
+    const long es = dtype == CVX_DT_F32 ? 4 : 2, eo = all.held != kX16 ? 1 : es;
+    const long nvec = (all.c + 16 / es - 1) / (16 / es);
+    const long most = all.held != kX16 ? 1l << 20 : nvec < (1l << 31) ? (1l << 31) / nvec : 1;
+    for (long r0 = 0; r0 < all.rows; r0 += most) {
+        GateArgs a = all;
+        a.rows = (int)(all.rows - r0 < most ? all.rows - r0 : most);
+        a.gate = static_cast<const char*>(all.gate) + r0 * all.gs * es;
+        if (all.up) a.up = static_cast<const char*>(all.up) + r0 * all.us * es;
+        a.y = static_cast<char*>(all.y) + r0 * all.ys * eo;
+        if (all.held != kX16) a.y_scale = all.y_scale + r0;
+        const hipError_t e = dtype == CVX_DT_F32   ? launch_t<float>(a, s)
+                             : dtype == CVX_DT_F16 ? launch_t<half_t>(a, s)
+                                                   : launch_t<bf16_t>(a, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace cvx

@@ -2,8 +2,8 @@
 // output, the row's scale, in one pass over the data.
 //
 //     h = x + r,  q = 1/sqrt(mean(h^2) + eps),  y = h*gamma*q
-//     8 bits: u = h*gamma, t = max|u|, code = nearest(u*(M/t)), scale = t*q/M,
-//     M = 448 (e4m3) or 127 (integers)
+//     8 bits: u = h*gamma, t = max|u|, code = nearest(u*f), scale = t*q/M,
+//     e4m3: M = 448, f = M/t; integers: M = 127, f = M*(1/t)
 //
 // t does not depend on q, so the sum of squares and the maximum are one
 // reduction: a row costs one exchange between its threads.  TPR threads hold a
@@ -19,7 +19,7 @@
 // The arithmetic is in 64 bits: the kernel is bound by memory, a 64-bit multiply
 // issues at the rate of a 32-bit one here, rows whose squares leave fp32's range
 // stay right (h itself is an fp32 sum, but for the one form below), and a code is
-// the nearest value to u*(M/t) itself, not to an fp32 neighbour of it.
+// the nearest value to u*f itself, not to an fp32 neighbour of it.
 //
 // Measured: 16384 rows of 4096 bf16 channels with residual and sum to e4m3 86 us,
 // 5.4 TB/s, the rate of a copy of that size; 96 rows of 8192 fp16 channels 4.2 us
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_rmsnorm(RmsArgs a)
 
     double f = q;
     if constexpr (OUT8) {
-        f = top > 0.0 ? kTop<OUT> / top : 0.0;
+        f = !(top > 0.0) ? 0.0 : OUT == kXI8 ? kTop<OUT> * (1.0 / top) : kTop<OUT> / top;
         // an infinity's row (q = 0) has a NaN scale, also where gamma hides it from `top`
         if (lane == 0) a.y_scale[row] = q > 0.0 ? (float)(top * q / kTop<OUT>) : __builtin_nanf("");
     }

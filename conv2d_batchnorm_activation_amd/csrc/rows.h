@@ -45,8 +45,10 @@ __device__ __forceinline__ float to_odd(double v)
 template <int OUT>
 __device__ __forceinline__ unsigned code_part(double v)
 {
+#pragma clang fp contract(off)  // v is a rounded product: fused into the sum, borders would be missed by a hair
     if constexpr (OUT == kXE4m3) return __builtin_bit_cast(unsigned, to_odd(v));
-    return (unsigned)__builtin_bit_cast(unsigned long long, v + 0x1.8p52);
+    const double at_ones = v + 0x1.8p52;
+    return (unsigned)__builtin_bit_cast(unsigned long long, at_ones);
 }
 template <int OUT>
 __device__ __forceinline__ unsigned pack_codes(unsigned a, unsigned b, unsigned c, unsigned d)

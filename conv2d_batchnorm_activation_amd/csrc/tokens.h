@@ -34,6 +34,19 @@ struct RmsArgs {
 };
 hipError_t launch_rmsnorm(const RmsArgs& a, int dtype, hipStream_t s);
 
+// ------------------------------------------------------ the gated activation
+struct GateArgs {
+    const void* gate;
+    const void* up;       // or null
+    void* y;
+    float* y_scale;       // 8-bit output only
+    long gs, us, ys;      // row strides, elements
+    int rows, c;
+    int act;
+    int held;             // y: kX16 for dtype, or an 8-bit type
+};
+hipError_t launch_gate(const GateArgs& a, int dtype, hipStream_t s);
+
 // ------------------------------------------------------------ the projection
 struct LinArgs {
     const void* x;

@@ -57,6 +57,11 @@ class cvx_rmsnorm_desc(ctypes.Structure):
         [(f, ctypes.c_long) for f in ("x_stride", "res_stride", "sum_stride", "y_stride")]
 
 
+class cvx_gate_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("rows", "c", "dtype", "out_dtype", "act")] + \
+        [(f, ctypes.c_long) for f in ("gate_stride", "up_stride", "y_stride")]
+
+
 class cvx_linear_desc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in
                 ("tokens", "c_in", "c_out", "dtype", "x_dtype", "act", "res_mode", "rank", "n_adapters")] + \
@@ -69,6 +74,7 @@ _Z = ctypes.c_size_t
 _DP = ctypes.POINTER(cvx_conv_desc)
 _LP = ctypes.POINTER(cvx_layer)
 _RP = ctypes.POINTER(cvx_rmsnorm_desc)
+_AP = ctypes.POINTER(cvx_gate_desc)
 _NP = ctypes.POINTER(cvx_linear_desc)
 
 lib.cvx_status_str.argtypes = [_I]
@@ -112,6 +118,8 @@ lib.cvx_conv_bn_act_nhwc.argtypes = [_DP, _I, _P, _P, _P, _P, _P, _P, _P]
 lib.cvx_conv_bn_act_nhwc.restype = _I
 lib.cvx_rmsnorm.argtypes = [_RP, _P, _P, _P, _P, _P, _P, _P]
 lib.cvx_rmsnorm.restype = _I
+lib.cvx_gate.argtypes = [_AP, _P, _P, _P, _P, _P]
+lib.cvx_gate.restype = _I
 lib.cvx_linear_workspace_bytes.argtypes = [_NP]
 lib.cvx_linear_workspace_bytes.restype = _Z
 lib.cvx_linear_plan.argtypes = [_NP, ctypes.c_char_p, _I]
@@ -130,7 +138,7 @@ EXPORTS = ("cvx_status_str", "cvx_version", "cvx_conv_out_shape", "cvx_conv_plan
            "cvx_conv_workspace_bytes", "cvx_packed_weights_bytes", "cvx_pack_weights", "cvx_fold_bn", "cvx_conv_bn_act", "cvx_preprocess_u8",
            "cvx_gap_fc", "cvx_forward_out_shape", "cvx_forward_workspace_bytes", "cvx_forward_plan",
            "cvx_forward", "cvx_nhwc_packed_weights_bytes", "cvx_nhwc_plan", "cvx_nhwc_pack_weights",
-           "cvx_conv_bn_act_nhwc", "cvx_rmsnorm", "cvx_linear_workspace_bytes", "cvx_linear_plan", "cvx_linear",
+           "cvx_conv_bn_act_nhwc", "cvx_rmsnorm", "cvx_gate", "cvx_linear_workspace_bytes", "cvx_linear_plan", "cvx_linear",
            "cvx_static_scratch_bytes", "cvx_forward_noalloc",
            "cvx_workgroup_xcds")
 
@@ -382,6 +390,22 @@ def cvx_rmsnorm(desc: cvx_rmsnorm_desc, x, residual, gamma, sum_out, y, y_scale=
                            _operand(gamma, _F32, dev, "gamma"), _operand(sum_out, held, dev, "sum_out"),
                            _operand(y, _HELD.get(desc.out_dtype), dev, "y"), _operand(y_scale, _F32, dev, "y_scale"),
                            _stream_on(dev, stream)), "cvx_rmsnorm")
+
+
+def make_gate_desc(rows, c, dtype, out_dtype=None, act=CVX_ACT_SILU, gate_stride=0, up_stride=0,
+                   y_stride=0) -> cvx_gate_desc:
+    return cvx_gate_desc(rows, c, dtype, dtype if out_dtype is None else out_dtype, act, gate_stride, up_stride,
+                         y_stride)
+
+
+def cvx_gate(desc: cvx_gate_desc, gate, up, y, y_scale=None, stream=None) -> None:
+    dev = _device(gate)
+    if _elsewhere(dev, cvx_gate, desc, gate, up, y, y_scale, stream):
+        return
+    held = _HELD.get(desc.dtype)
+    _check(lib.cvx_gate(ctypes.byref(desc), _operand(gate, held, dev, "gate"), _operand(up, held, dev, "up"),
+                        _operand(y, _HELD.get(desc.out_dtype), dev, "y"), _operand(y_scale, _F32, dev, "y_scale"),
+                        _stream_on(dev, stream)), "cvx_gate")
 
 
 def make_linear_desc(tokens, c_in, c_out, dtype, x_dtype=None, act=CVX_ACT_NONE, res_mode=CVX_RES_NONE, rank=0,

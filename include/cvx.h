@@ -339,9 +339,10 @@ CVX_API cvx_status cvx_conv_bn_act_nhwc(const cvx_conv_desc *d, int dtype, const
 /* ------------------------------------------------ operators on tokens
  * A channels-last tensor with its pixels as rows, [rows][channels]: a 1x1 layer
  * is then a projection of every row, and the rows may as well be the tokens of
- * a sequence model.  The two operators here are such a projection in 16 or 8
- * bits, with low-rank adapters for many requests at once, and the norm between
- * projections, whose 8-bit output with a scale per row the projection reads.
+ * a sequence model.  The operators here are such a projection in 16 or 8 bits, with
+ * low-rank adapters for many requests at once, the same grouped by expert, and the
+ * norm and the gated activation between projections, whose 8-bit output with a scale
+ * per row the projections read.
  * Rows may lie further apart than they are wide (a `*_stride` of the
  * descriptor, in elements; 0 = dense), so a slice of a wider tensor's channels
  * is an operand as it is.  Where two operands must not overlap, what counts is
@@ -373,7 +374,8 @@ typedef struct cvx_rmsnorm_desc {
  * nearest to its value, and only `sum` can overflow.  With 8-bit output,
  * u_i = h_i*gamma_i, t = max_i |u_i| and M = 448 (e4m3) or 127 (integers),
  *     y_i = code(u_i * (M/t)),  y_scale = t*q/M         (t = 0: zeros)
- * the nearest e4m3 value or integer (ties to even; -128 is never one), so that
+ * the nearest e4m3 value or integer (ties to even; -128 is never one; for integers
+ * M/t is 127 * (1/t), every step rounded to 64 bits, which decides at borders), so that
  * y_i * y_scale is the norm's output; q, which depends on the whole row's sum,
  * cancels in the codes.
  * A row that holds a NaN gives NaN throughout (8 bits: a NaN scale); one that
@@ -393,6 +395,40 @@ typedef struct cvx_rmsnorm_desc {
  */
 CVX_API cvx_status cvx_rmsnorm(const cvx_rmsnorm_desc *d, const void *x, const void *residual,
                                const float *gamma, void *sum, void *y, float *y_scale, void *stream);
+
+typedef struct cvx_gate_desc {
+    int rows, c;        /* gate and up [rows][c]; both at least 1, c at most 2^30 */
+    int dtype;          /* CVX_DT_F32, _F16 or _BF16: gate, up                    */
+    int out_dtype;      /* type of y: dtype, CVX_DT_E4M3 or CVX_DT_I8             */
+    int act;            /* CVX_ACT_*                                              */
+    long gate_stride, up_stride, y_stride; /* row strides, 0 or >= c              */
+} cvx_gate_desc;
+
+/*
+ * cvx_gate -- the gated activation between the two products of a layer, one launch:
+ *     u = act(gate) * up          (u = act(gate) without `up`)
+ * and y = u, taken in fp32 and rounded once; or, with 8-bit output, t = max_i |u_i| of
+ * the row and M = 448 (e4m3) or 127 (integers),
+ *     y_i = code(u_i * (M * (1/t))),  y_scale = t/M     (t = 0: zeros)
+ * every step in 64 bits: the nearest e4m3 value or integer, ties to even, as cvx_rmsnorm
+ * writes them and cvx_linear reads them.  With CVX_ACT_NONE and no `up`, rows are
+ * brought to 8 bits as they are.  gate and up may be halves of one tensor, the output
+ * of a product with both weights.
+ * Values are as the formula gives them (max(0, NaN) and 0 * infinity are NaN, SiLU of
+ * the lowest infinity too).  With 8-bit output a row that holds a NaN or an infinity,
+ * or gives one, has a NaN scale; other rows are not touched by it.
+ *   gate, up : device [rows][c] of dtype, aligned to an element; up may be NULL, and may
+ *              equal gate.
+ *   y        : device [rows][c] of out_dtype, aligned to an element.
+ *   y_scale  : device fp32 [rows]; required iff out_dtype is an 8-bit type.
+ * y and y_scale must not overlap each other or an input.
+ * Rows aligned to 16 bytes are fastest; others give the same results.
+ * Errors: CVX_ERR_NULL, CVX_ERR_SHAPE (rows or c < 1, c > 2^30, a stride between 0
+ * and c, more than 2^40 elements from first to last), CVX_ERR_ARG (types, act),
+ * CVX_ERR_ALIGN, CVX_ERR_ALIAS, CVX_ERR_HIP.
+ */
+CVX_API cvx_status cvx_gate(const cvx_gate_desc *d, const void *gate, const void *up, void *y, float *y_scale,
+                            void *stream);
 
 typedef struct cvx_linear_desc {
     int tokens;         /* rows of x and y, 1 to 2^24                             */

@@ -1,7 +1,7 @@
 """8-bit integers: the codes cvx_rmsnorm writes and the projection cvx_linear makes of such
 codes, against their definitions in 64 bits, element by element.
 
-Tolerances.  A code is the integer nearest to u*(127/t), taken in 64 bits on both sides by
+Tolerances.  A code is the integer nearest to u*(127*(1/t)), taken in 64 bits on both sides by
 the same operations, so codes are equal.  y_scale is a 64-bit value rounded to fp32, 2^-24,
 and the definition's own 64-bit roundings are far below that; 2^-23 is allowed.  Sums of
 products of integers are exact; rounded to fp32 (2^-24), they take two scales, the bias,
@@ -35,7 +35,7 @@ def setup_module(module):
 def codes_of(u, most=127.0):
     """(codes, the rows' largest magnitudes) of rows in 64 bits."""
     t = u.abs().amax(1)
-    return torch.round(u * torch.where(t > 0, most / t, 0.0)[:, None]), t
+    return torch.round(u * torch.where(t > 0, most * (1.0 / t), 0.0)[:, None]), t
 
 
 def norm_of(x, r, g):
@@ -83,6 +83,18 @@ def test_norm_ties_and_limits():
     say("norm to integers: ties")
     cvx.cvx_rmsnorm(cvx.make_rmsnorm_desc(1, 8, F32, I8, EPS), x.to(DEV), None, torch.ones(8, device=DEV), None, y, q)
     assert y.cpu().tolist()[0] == [127, 64, -64, -127, 0, 3, 1, 127]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_norm_borders(dt):
+    # multiples of few values: many u*127/t lie at a border, or a rounding off it
+    g = torch.Generator().manual_seed(3)
+    x = torch.randint(-256, 257, (2000, 700), generator=g).to(DT[dt])
+    y = torch.empty(2000, 700, dtype=torch.int8, device=DEV)
+    q = torch.empty(2000, device=DEV)
+    say("norm to integers: borders")
+    cvx.cvx_rmsnorm(cvx.make_rmsnorm_desc(2000, 700, dt, I8, EPS), x.to(DEV), None, torch.ones(700, device=DEV), None, y, q)
+    assert torch.equal(y.cpu().double(), norm_of(x, None, torch.ones(700))[0])
 
 
 def test_norm_bad_rows():
