@@ -7,9 +7,11 @@
 // Bound by memory: every value is read once and written once.  With 8-bit output a
 // row's largest magnitude is one reduction between the TPR threads that hold it, as NV
 // 16-byte vectors an operand each; rows too long to be held (NV = 0) are read a second
-// time.  u is then taken and held in 64 bits, so that a code is the nearest to its
-// value and integers do not depend on how the exponential was rounded: some 35 64-bit
-// instructions a value, issued at the rate of 32-bit ones.  Otherwise u is in fp32
+// time.  t and the codes are those of 64-bit values, so that a code is the nearest to
+// its value and integers do not depend on how an exponential was rounded.  Few values
+// need 64 bits for that: those that may be the largest, and those that fp32 leaves at a
+// border between two codes.  With 64 bits for all (some 35 instructions a value) 8192
+// rows of 14336 bf16 channels took 236 us; they take 112, 5.2 TB/s.  Output of the inputs' type is u in fp32,
 // and there is no row: a thread takes a vector.
 #include <type_traits>
 
@@ -58,35 +60,70 @@ __device__ __forceinline__ double act64(double g)
     return g;
 }
 
-template <int ACT>
+// In fp32.  FAST: by the hardware's exponential and reciprocal.  Of the exponential's
+// argument, -g*log2(e), the rounding leaves up to |g|*2^-24 of the result, so that it is
+// good to 2^-20 or so of the value where g is at least kDeep.
+constexpr float kDeep = -16.0f;
+template <int ACT, bool FAST>
 __device__ __forceinline__ float act32(float g)
 {
     if constexpr (ACT == CVX_ACT_RELU) return g < 0.0f ? 0.0f : g;
+    if constexpr (ACT == CVX_ACT_SILU && FAST)
+        return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.442695041f));
     if constexpr (ACT == CVX_ACT_SILU) return g / (1.0f + expf(-g));
     return g;
 }
 
 // VEC values of an operand from channel i0, zero past c.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, int i0, int c, float (&o)[VEC])
+__device__ __forceinline__ typename Vec<T, VEC>::type load_vec(const T* p, int i0, int c)
 {
     typedef typename Vec<T, VEC>::type V;
-    if (i0 + VEC <= c) {
-        const V v = *reinterpret_cast<const V*>(p + i0);
+    if (i0 + VEC <= c) return *reinterpret_cast<const V*>(p + i0);
+    V v;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = (float)v[e];
-    } else {
+    for (int e = 0; e < VEC; ++e) v[e] = i0 + e < c ? p[i0 + e] : (T)0.0f;
+    return v;
+}
+
+// The codes of VEC values u*f, from fp32; true if one of them may be another, u being
+// off by less than kOff of itself, none larger than `most`.
+constexpr float kOff = 0x1p-19f;
+template <int OUT, int VEC>
+__device__ __forceinline__ bool codes32(const float (&u)[VEC], float most, float f, unsigned (&w)[VEC / 4])
+{
+    if constexpr (OUT == kXE4m3) {  // the same codes from a little less and a little more
+        const float less = f * (1.0f - kOff), more = f * (1.0f + kOff);
+        bool any = false;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = i0 + e < c ? (float)p[i0 + e] : 0.0f;
+        for (int q = 0; q < VEC; q += 4) {
+            w[q / 4] = pack_e4m3(u[q] * less, u[q + 1] * less, u[q + 2] * less, u[q + 3] * less);
+            any |= w[q / 4] != pack_e4m3(u[q] * more, u[q + 1] * more, u[q + 2] * more, u[q + 3] * more);
+        }
+        return any;
     }
+    unsigned ones[VEC];  // a sum that leaves none below one
+    float off = 0.0f;    // the most that a value is off its integer
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const float s = fmaf(u[e], f, 0x1.8p23f);
+        ones[e] = __builtin_bit_cast(unsigned, s);
+        off = fmaxf(off, fabsf(fmaf(u[e], f, 0x1.8p23f - s)));
+    }
+#pragma unroll
+    for (int q = 0; q < VEC; q += 4)
+        w[q / 4] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(ones[q + 3], ones[q + 2], 0x0c0c0400u),
+                                         __builtin_amdgcn_perm(ones[q + 1], ones[q], 0x0c0c0400u), 0x05040100u);
+    return off > 0.5f - (most * f + 1.0f) * kOff;
 }
 
 // 8-bit output: TPR threads a row.
 template <typename T, int TPR, int NV, int ACT, bool UP, int OUT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_gate(GateArgs a)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 1) k_gate(GateArgs a)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
     constexpr int HOLD = NV > 0 ? NV : 1;
+    typedef typename Vec<T, VEC>::type V;
     const int lane = threadIdx.x % TPR;
     const long row = TPR < 256 ? (long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR : (long)blockIdx.x;
     if (row >= a.rows) return;  // whole waves: a row has at least one
@@ -95,63 +132,88 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k_gate(GateArgs a)
     unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.ys;
     const int c = a.c, nvec = (c + VEC - 1) / VEC;
 
-    float gv[HOLD][VEC], uv[UP ? HOLD : 1][VEC];
+    V gv[HOLD], uv[UP ? HOLD : 1];
     auto load = [&](int v, int j) {
-        load_vec<T, VEC>(g, v * VEC, c, gv[j]);
-        if constexpr (UP) load_vec<T, VEC>(p, v * VEC, c, uv[UP ? j : 0]);
+        gv[j] = load_vec<T, VEC>(g, v * VEC, c);
+        if constexpr (UP) uv[UP ? j : 0] = load_vec<T, VEC>(p, v * VEC, c);
     };
-    auto value = [&](int j, int e) {
-        const double u = act64<ACT>((double)gv[j][e]);
-        return UP ? u * (double)uv[UP ? j : 0][e] : u;
+    auto exact = [&](int j, int e) {
+        const double x = act64<ACT>((double)(float)gv[j][e]);
+        return UP ? x * (double)(float)uv[UP ? j : 0][e] : x;
     };
-    double held[HOLD][VEC], top = 0.0, odd = 0.0;
-    auto look = [&](int j) {
+    // calls f(vector's index, its slot) for every vector of this thread, loaded before
+    auto each = [&](auto f) {
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (lane + j * TPR < nvec) f(lane + j * TPR, j);
+        } else {
+            for (int v = lane; v < nvec; v += TPR) {
+                load(v, 0);
+                f(v, 0);
+            }
+        }
+    };
+    // a vector's u in fp32 and the largest of them: infinite where fp32 does not tell
+    float u[HOLD][VEC], most[HOLD];
+    auto near = [&](int j) {
+        float m = 0.0f, low = 0.0f, odd = 0.0f;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            held[j][e] = value(j, e);
-            top = fmax(top, fabs(held[j][e]));
-            odd = fma(held[j][e], 0.0, odd);  // a NaN from the first NaN or infinity on
+            const float gf = (float)gv[j][e];
+            u[j][e] = act32<ACT, true>(gf);
+            if constexpr (UP) u[j][e] *= (float)uv[UP ? j : 0][e];
+            low = fminf(low, gf);
+            m = fmaxf(m, fabsf(u[j][e]));
+            if (e % 2) odd = fmaf(u[j][e], u[j][e - 1], odd);  // a NaN or an infinity from either on
         }
+        const bool told = fabsf(odd) < __builtin_inff() && (ACT != CVX_ACT_SILU || low >= kDeep);
+        most[j] = told ? m : __builtin_inff();
     };
-    if constexpr (NV > 0) {
+    float top = 0.0f;
+    if constexpr (NV > 0) each([&](int v, int j) { load(v, j); });
+    each([&](int, int j) {
+        near(j);
+        top = fmaxf(top, most[j] < __builtin_inff() ? most[j] : 0.0f);
+    });
+    top = row_max<TPR>(top);
+
+    // t, in 64 bits: the largest of the vectors that may hold it, those that fp32 does
+    // not tell among them
+    const bool wide = !(top > 0x1p-60f && top < 0x1p100f);  // all may
+    const float least = top * (1.0f - kOff);
+    double t = 0.0, bad = 0.0;
+    each([&](int, int j) {
+        if constexpr (NV == 0) near(j);
+        if (!wide && most[j] < least) return;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (lane + j * TPR < nvec) load(lane + j * TPR, j);
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (lane + j * TPR < nvec) look(j);
-    } else {
-        for (int v = lane; v < nvec; v += TPR) {
-            load(v, 0);
-            look(0);
+        for (int e = 0; e < VEC; ++e) {
+            const double x = exact(j, e);
+            t = fmax(t, fabs(x));
+            bad = fma(x, 0.0, bad);
         }
-    }
-    if (odd != 0.0) top = __builtin_inf();
+    });
+    if (bad != 0.0) t = __builtin_inf();
     double none = 0.0;
-    row_reduce<TPR, true>(none, top);
-    const bool bad = top > 1.7e308;
-    const double f = top > 0.0 && !bad ? kTop<OUT> * (1.0 / top) : 0.0;
-    if (lane == 0) a.y_scale[row] = bad ? __builtin_nanf("") : (float)(top / kTop<OUT>);
-    auto put = [&](int v, int j) {
-        unsigned u[VEC], w[VEC / 4];
+    row_reduce<TPR, true>(none, t);
+    const bool lost = t > 1.7e308;
+    const double f = t > 0.0 && !lost ? kTop<OUT> * (1.0 / t) : 0.0;
+    if (lane == 0) a.y_scale[row] = lost ? __builtin_nanf("") : (float)(t / kTop<OUT>);
+
+    // codes from fp32 where it tells them, else from 64 bits
+    each([&](int v, int j) {
+        unsigned w[VEC / 4];
+        if constexpr (NV == 0) near(j);
+        bool any = codes32<OUT, VEC>(u[j], most[j], (float)f, w);
+        if (any || wide || most[j] == __builtin_inff()) {
+            unsigned x[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) u[e] = code_part<OUT>(held[j][e] * f);
+            for (int e = 0; e < VEC; ++e) x[e] = code_part<OUT>(exact(j, e) * f);
 #pragma unroll
-        for (int q = 0; q < VEC / 4; ++q) w[q] = pack_codes<OUT>(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
-        store_codes<VEC>(y, v * VEC, c, w);
-    };
-    if constexpr (NV > 0) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (lane + j * TPR < nvec) put(lane + j * TPR, j);
-    } else {
-        for (int v = lane; v < nvec; v += TPR) {
-            load(v, 0);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) held[0][e] = value(0, e);
-            put(v, 0);
+            for (int q = 0; q < VEC / 4; ++q) w[q] = pack_codes<OUT>(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
         }
-    }
+        store_codes<VEC>(y, v * VEC, c, w);
+    });
 }
 
 // Output of the inputs' type: a thread a vector.
@@ -165,13 +227,14 @@ __global__ void __launch_bounds__(256) k_gate_wide(GateArgs a)
     const long row = at / nvec;
     const int i0 = (int)(at - row * nvec) * VEC, c = a.c;
     if (row >= a.rows) return;
-    float g[VEC], u[VEC];
-    load_vec<T, VEC>(static_cast<const T*>(a.gate) + row * a.gs, i0, c, g);
-    if constexpr (UP) load_vec<T, VEC>(static_cast<const T*>(a.up) + row * a.us, i0, c, u);
+    const V gv = load_vec<T, VEC>(static_cast<const T*>(a.gate) + row * a.gs, i0, c);
+    V uv;
+    if constexpr (UP) uv = load_vec<T, VEC>(static_cast<const T*>(a.up) + row * a.us, i0, c);
+    float g[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        g[e] = act32<ACT>(g[e]);
-        if constexpr (UP) g[e] *= u[e];
+        g[e] = act32<ACT, false>((float)gv[e]);
+        if constexpr (UP) g[e] *= (float)uv[e];
     }
     T* y = static_cast<T*>(a.y) + row * a.ys;
     if (i0 + VEC <= c) {

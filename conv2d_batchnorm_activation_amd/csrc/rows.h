@@ -106,6 +106,29 @@ __device__ __forceinline__ double wave_all(double v, OP op)
     return op(op(lane_value<0>(v), lane_value<16>(v)), op(lane_value<32>(v), lane_value<48>(v)));
 }
 
+// The largest of the row's TPR threads' values, none of them a NaN.
+template <int TPR>
+__device__ __forceinline__ float row_max(float v)
+{
+    auto bits = [](float f) { return __builtin_bit_cast(int, f); };
+    auto value = [](int i) { return __builtin_bit_cast(float, i); };
+    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0xb1, 0xf, 0xf, true)));
+    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0x4e, 0xf, 0xf, true)));
+    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0x141, 0xf, 0xf, true)));
+    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0x140, 0xf, 0xf, true)));
+    auto lane = [&](int l) { return value(__builtin_amdgcn_readlane(bits(v), l)); };
+    v = fmaxf(fmaxf(lane(0), lane(16)), fmaxf(lane(32), lane(48)));
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        __shared__ float lv[W];
+        if ((threadIdx.x & 63) == 0) lv[threadIdx.x >> 6] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) v = fmaxf(v, lv[i]);
+    }
+    return v;
+}
+
 // Row sums over TPR threads of `s` and maxima of `m`; every thread gets both.
 template <int TPR, bool MAX>
 __device__ __forceinline__ void row_reduce(double& s, double& m)

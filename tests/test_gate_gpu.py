@@ -160,6 +160,35 @@ def test_the_widest_ranges():
     assert got[2, 0] == 0 and got[2, 1] == 800 and got[2, 3] == 0 and got[0, 0] == float("inf")
 
 
+@pytest.mark.parametrize("c", [64, 2000, 14336, 40000])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_rows_of_mixed_sizes(c, dt):
+    # gates far below zero beside factors that make up for it, rows of tiny and of huge values,
+    # rows whose largest value is one of those
+    r = torch.Generator().manual_seed(c)
+    g, p = 6 * torch.randn(12, c, generator=r), torch.randn(12, c, generator=r)
+    g[1, ::7], p[1, ::7] = -30.0, 1e12
+    g[2, c // 2], p[2, c // 2] = -70.0, 1e30
+    g[3], p[3] = g[3] * 1e-10, p[3] * 1e-15
+    g[4], p[4] = g[4] * 1e18, p[4] * 1e15
+    g[5, 1:] = -60 - g[5, 1:].abs()
+    g[6], p[6] = -100.0, 1e20
+    g[7, 3], p[7, 3] = 1e15, 1e15
+    g, p = g.to(DT[dt]), p.to(DT[dt])
+    for out in (I8, E4M3):
+        check(g, p, dt, out, SILU)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_borders(dt):
+    # products of few values: many u*M/t lie at a border, or a rounding off it
+    r = torch.Generator().manual_seed(4)
+    g, p = (torch.randint(-256, 257, (1500, 700), generator=r).to(DT[dt]) for _ in range(2))
+    for out in (I8, E4M3):
+        check(g, p, dt, out, NONE)
+        check(g, None, dt, out, RELU)
+
+
 def test_far_rows_streams_and_graphs():
     # two rows 3 GB apart
     far, c = 3 << 29, 1000
