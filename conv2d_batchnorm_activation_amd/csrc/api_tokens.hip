@@ -73,6 +73,24 @@ cvx_status check_linear(const cvx_linear_desc* d, long* xs, long* rs, long* ys)
     return CVX_OK;
 }
 
+cvx_status check_grouped(const cvx_grouped_desc* d, long* xs, long* ys)
+{
+    if (d == nullptr) return CVX_ERR_NULL;
+    if (!dtype16(d->dtype) || (d->x_dtype != d->dtype && !dtype8(d->x_dtype))) return CVX_ERR_ARG;
+    if (d->act < CVX_ACT_NONE || d->act > CVX_ACT_SILU) return CVX_ERR_ARG;
+    if (d->rows < 1 || d->tokens < 1 || d->c_in < 1 || d->c_out < 1 || d->rows > kMaxTokens || d->tokens > kMaxTokens ||
+        d->c_in > kMaxChannels || d->c_out > kMaxChannels || (long)d->rows * d->c_out > kMaxOut)
+        return CVX_ERR_SHAPE;
+    if (d->n_groups < 1 || d->n_groups > kMaxGroups || (long)d->n_groups * d->c_out > kMaxSpan / d->c_in)
+        return CVX_ERR_SHAPE;
+    if (!stride_of(d->x_stride, d->c_in, d->tokens, xs) || *xs > kMaxPitch) return CVX_ERR_SHAPE;
+    if (!stride_of(d->y_stride, d->c_out, d->rows, ys) || *ys > kMaxPitch) return CVX_ERR_SHAPE;
+    if (d->x_dtype == CVX_DT_I8 && d->c_in > kMaxI8) return CVX_ERR_SHAPE;
+    const int per = dtype8(d->x_dtype) ? 16 : 8;
+    if (d->c_in % per != 0 || *xs % per != 0 || d->c_out % 4 != 0 || *ys % 4 != 0) return CVX_ERR_UNSUPPORTED;
+    return CVX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -249,6 +267,68 @@ cvx_status cvx_linear(const cvx_linear_desc* d, const void* x, const float* x_sc
     if (lora && !p.one && launch_lora_down(a, p, d->dtype, held, s) != hipSuccess) return CVX_ERR_HIP;
     if (p.join && launch_lora_join(a, d->dtype, s) != hipSuccess) return CVX_ERR_HIP;
     const hipError_t e = p.few ? launch_linear_few(a, p, d->dtype, held, s) : launch_linear_tile(a, p, d->dtype, held, s);
+    return e == hipSuccess ? CVX_OK : CVX_ERR_HIP;
+}
+
+cvx_status cvx_linear_grouped_plan(const cvx_grouped_desc* d, char* buf, int buf_len)
+{
+    if (buf == nullptr || buf_len < 1) return CVX_ERR_NULL;
+    long xs, ys;
+    const cvx_status st = check_grouped(d, &xs, &ys);
+    if (st != CVX_OK) return st;
+    grouped_describe(*d, grouped_plan(*d), buf, buf_len);
+    return CVX_OK;
+}
+
+cvx_status cvx_linear_grouped(const cvx_grouped_desc* d, const void* x, const float* x_scale, const void* w,
+                              const float* scale, const float* bias, const int* offset, const int* row_id,
+                              const float* row_weight, void* y, void* stream)
+{
+    GroupArgs a;
+    const cvx_status st = check_grouped(d, &a.xs, &a.ys);
+    if (st != CVX_OK) return st;
+    const bool x8 = dtype8(d->x_dtype);
+    const long ex = dt_bytes(d->x_dtype);
+    // rows found by their number lie at 32-bit offsets, as many as stay below kOOB
+    if (row_id ? ((d->tokens - 1) * a.xs + d->c_in) * ex > (1l << 31) : d->tokens < d->rows) return CVX_ERR_SHAPE;
+    if (!x || !w || !y || !offset || (x8 && !x_scale)) return CVX_ERR_NULL;
+    a.x = x;
+    a.x_scale = x8 ? x_scale : nullptr;
+    a.w = w;
+    a.scale = scale;
+    a.bias = bias;
+    a.offset = offset;
+    a.row_id = row_id;
+    a.weight = row_weight;
+    a.y = y;
+    if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(y, 8) || !aligned_to(a.x_scale, 4) ||
+        !aligned_to(scale, 4) || !aligned_to(bias, 4) || !aligned_to(offset, 4) || !aligned_to(row_id, 4) ||
+        !aligned_to(row_weight, 4))
+        return CVX_ERR_ALIGN;
+    const Span ysp = rows_span(y, d->rows, a.ys, d->c_out, 2);
+    const size_t outs = (size_t)d->n_groups * d->c_out;
+    const struct {
+        const void* p;
+        Span s;
+    } in[] = {{x, rows_span(x, d->tokens, a.xs, d->c_in, (unsigned)ex)},
+              {a.x_scale, bytes_span(a.x_scale, 4ul * d->tokens)},
+              {w, bytes_span(w, outs * d->c_in * ex)},
+              {scale, bytes_span(scale, 4 * outs)},
+              {bias, bytes_span(bias, 4 * outs)},
+              {offset, bytes_span(offset, 4ul * d->n_groups + 4)},
+              {row_id, bytes_span(row_id, 4ul * d->rows)},
+              {row_weight, bytes_span(row_weight, 4ul * d->rows)}};
+    for (const auto& i : in)
+        if (i.p && meets(ysp, i.s)) return CVX_ERR_ALIAS;
+    a.rows = d->rows;
+    a.tokens = d->tokens;
+    a.groups = d->n_groups;
+    a.cin = d->c_in;
+    a.cout = d->c_out;
+    a.act = d->act;
+    a.tiles_m = 0;
+    const hipError_t e = launch_linear_grouped(a, grouped_plan(*d), d->dtype, held_of(d->dtype, d->x_dtype),
+                                               static_cast<hipStream_t>(stream));
     return e == hipSuccess ? CVX_OK : CVX_ERR_HIP;
 }
 

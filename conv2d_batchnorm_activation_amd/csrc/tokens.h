@@ -100,4 +100,32 @@ hipError_t launch_lora_join(const LinArgs& a, int dtype, hipStream_t s);
 hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s);
 hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s);
 
+// ------------------------------------------------- products grouped by expert
+constexpr int kMaxGroups = 1024;  // their first tiles and rows stand in LDS
+
+struct GroupArgs {
+    const void* x;
+    const float* x_scale;  // 8-bit x only
+    const void* w;
+    const float* scale;    // or null
+    const float* bias;     // or null
+    const int* offset;
+    const int* row_id;     // or null
+    const float* weight;   // or null
+    void* y;
+    long xs, ys;           // row strides, elements
+    int rows, tokens, groups, cin, cout;
+    int act;
+    int tiles_m;           // tiles of output channels
+};
+
+struct GroupPlan {
+    int mb, nb;            // tile: 64*mb channels x 64*nb rows
+    int grid;              // workgroups, a multiple of eight
+};
+
+GroupPlan grouped_plan(const cvx_grouped_desc& d);
+void grouped_describe(const cvx_grouped_desc& d, const GroupPlan& p, char* buf, int len);
+hipError_t launch_linear_grouped(const GroupArgs& a, const GroupPlan& p, int dtype, int held, hipStream_t s);
+
 }  // namespace cvx

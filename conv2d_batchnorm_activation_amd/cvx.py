@@ -68,6 +68,12 @@ class cvx_linear_desc(ctypes.Structure):
         [(f, ctypes.c_long) for f in ("x_stride", "res_stride", "y_stride")]
 
 
+class cvx_grouped_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in
+                ("rows", "tokens", "n_groups", "c_in", "c_out", "dtype", "x_dtype", "act")] + \
+        [(f, ctypes.c_long) for f in ("x_stride", "y_stride")]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
@@ -76,6 +82,7 @@ _LP = ctypes.POINTER(cvx_layer)
 _RP = ctypes.POINTER(cvx_rmsnorm_desc)
 _AP = ctypes.POINTER(cvx_gate_desc)
 _NP = ctypes.POINTER(cvx_linear_desc)
+_GP = ctypes.POINTER(cvx_grouped_desc)
 
 lib.cvx_status_str.argtypes = [_I]
 lib.cvx_status_str.restype = ctypes.c_char_p
@@ -126,6 +133,10 @@ lib.cvx_linear_plan.argtypes = [_NP, ctypes.c_char_p, _I]
 lib.cvx_linear_plan.restype = _I
 lib.cvx_linear.argtypes = [_NP] + [_P] * 12 + [_Z, _P]
 lib.cvx_linear.restype = _I
+lib.cvx_linear_grouped_plan.argtypes = [_GP, ctypes.c_char_p, _I]
+lib.cvx_linear_grouped_plan.restype = _I
+lib.cvx_linear_grouped.argtypes = [_GP] + [_P] * 10
+lib.cvx_linear_grouped.restype = _I
 lib.cvx_static_scratch_bytes.argtypes = []
 lib.cvx_static_scratch_bytes.restype = _Z
 lib.cvx_forward_noalloc.argtypes = [_LP, _I, _P, _P, _P]
@@ -139,6 +150,7 @@ EXPORTS = ("cvx_status_str", "cvx_version", "cvx_conv_out_shape", "cvx_conv_plan
            "cvx_gap_fc", "cvx_forward_out_shape", "cvx_forward_workspace_bytes", "cvx_forward_plan",
            "cvx_forward", "cvx_nhwc_packed_weights_bytes", "cvx_nhwc_plan", "cvx_nhwc_pack_weights",
            "cvx_conv_bn_act_nhwc", "cvx_rmsnorm", "cvx_gate", "cvx_linear_workspace_bytes", "cvx_linear_plan", "cvx_linear",
+           "cvx_linear_grouped_plan", "cvx_linear_grouped",
            "cvx_static_scratch_bytes", "cvx_forward_noalloc",
            "cvx_workgroup_xcds")
 
@@ -442,3 +454,30 @@ def cvx_linear(desc: cvx_linear_desc, x, w, y, x_scale=None, scale=None, bias=No
                           _operand(lora_alpha, _F32, dev, "lora_alpha"), _operand(lora_id, _I32, dev, "lora_id"),
                           _operand(y, held, dev, "y"), _operand(workspace, None, dev, "workspace"), ws_bytes,
                           _stream_on(dev, stream)), "cvx_linear")
+
+
+def make_grouped_desc(rows, tokens, n_groups, c_in, c_out, dtype, x_dtype=None, act=CVX_ACT_NONE, x_stride=0,
+                      y_stride=0) -> cvx_grouped_desc:
+    return cvx_grouped_desc(rows, tokens, n_groups, c_in, c_out, dtype, dtype if x_dtype is None else x_dtype, act,
+                            x_stride, y_stride)
+
+
+def cvx_linear_grouped_plan(desc: cvx_grouped_desc) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.cvx_linear_grouped_plan(ctypes.byref(desc), buf, 256), "cvx_linear_grouped_plan")
+    return buf.value.decode()
+
+
+def cvx_linear_grouped(desc: cvx_grouped_desc, x, w, offset, y, x_scale=None, scale=None, bias=None, row_id=None,
+                       row_weight=None, stream=None) -> None:
+    dev = _device(x)
+    if _elsewhere(dev, cvx_linear_grouped, desc, x, w, offset, y, x_scale, scale, bias, row_id, row_weight, stream):
+        return
+    held_x = _HELD.get(desc.x_dtype)
+    _check(lib.cvx_linear_grouped(ctypes.byref(desc), _operand(x, held_x, dev, "x"),
+                                  _operand(x_scale, _F32, dev, "x_scale"), _operand(w, held_x, dev, "w"),
+                                  _operand(scale, _F32, dev, "scale"), _operand(bias, _F32, dev, "bias"),
+                                  _operand(offset, _I32, dev, "offset"), _operand(row_id, _I32, dev, "row_id"),
+                                  _operand(row_weight, _F32, dev, "row_weight"),
+                                  _operand(y, _HELD.get(desc.dtype), dev, "y"), _stream_on(dev, stream)),
+           "cvx_linear_grouped")

@@ -497,6 +497,55 @@ CVX_API cvx_status cvx_linear(const cvx_linear_desc *d, const void *x, const flo
                               const void *lora_a, const void *lora_b, const float *lora_alpha,
                               const int *lora_id, void *y, void *workspace, size_t ws_bytes, void *stream);
 
+typedef struct cvx_grouped_desc {
+    int rows;           /* rows of y, 1 to 2^24                                   */
+    int tokens;         /* rows of x, 1 to 2^24; without row_id at least `rows`   */
+    int n_groups;       /* 1 to 1024                                              */
+    int c_in, c_out;    /* channels, at most 2^20 each; rows * c_out at most 2^37,
+                         * and no operand more than 2^40 elements from first to last  */
+    int dtype;          /* CVX_DT_F16 or _BF16: y                                 */
+    int x_dtype;        /* type of x and w: dtype, CVX_DT_E4M3 or CVX_DT_I8       */
+    int act;            /* CVX_ACT_*                                              */
+    long x_stride, y_stride; /* row strides, 0 or >= the channels, at most 2^21   */
+} cvx_grouped_desc;
+
+/* Host-only query: the kernel and tile chosen for `d`, like cvx_conv_plan. */
+CVX_API cvx_status cvx_linear_grouped_plan(const cvx_grouped_desc *d, char *buf, int buf_len);
+
+/*
+ * cvx_linear_grouped -- projection of rows that are grouped by expert, every row by
+ * its group's weights, in one launch:
+ *     z_i[o] = scale[g][o] * x_scale[j] * sum_k w[g][o][k]*x[j][k] + bias[g][o]
+ *     y_i    = row_weight[i] * act(z_i)          j = row_id[i], or i without row_id
+ * for the rows i of group g, offset[g] <= i < offset[g+1].  Groups may have any number
+ * of rows, none among them.  Ends outside 0..rows are taken as the nearer of these, and
+ * one below an end before it as the largest before it.  Rows before the first group or
+ * behind the last are left as they are.  A row whose row_id is negative or not below
+ * `tokens` is taken as zeros.  Sums are those of cvx_linear: exact for 8-bit integers,
+ * else in fp32, with what it says of e4m3 operands where more than 16 rows a group come
+ * on average.  y is rounded once.  A group's weights, infinities and NaN included, reach
+ * its rows and no others, and so does a row of x; a NaN stays one through every
+ * activation.  Results do not depend on timing.
+ *   x         : device [tokens][c_in] of x_dtype, 16-byte aligned rows; with row_id, at
+ *               most 2^31 bytes from first to last.
+ *   x_scale   : device fp32 [tokens]; required iff x_dtype is an 8-bit type.
+ *   w         : device [n_groups][c_out][c_in] of x_dtype, dense, 16-byte aligned.
+ *   scale, bias: device fp32 [n_groups][c_out]; NULL means 1 and 0.
+ *   offset    : device int32 [n_groups + 1].
+ *   row_id    : device int32 [rows], or NULL.  A row of x may be named any number of times.
+ *   row_weight: device fp32 [rows], or NULL for 1.
+ *   y         : device [rows][c_out] of dtype, 8-byte aligned rows; must not overlap anything read.
+ * Supported: c_in and x_stride multiples of 8 (16 in 8 bits), c_out and y_stride
+ * multiples of 4; else CVX_ERR_UNSUPPORTED.
+ * Errors otherwise: CVX_ERR_NULL, CVX_ERR_SHAPE (sizes, strides, more than 2^17 - 16
+ * channels in of 8-bit integers), CVX_ERR_ARG (types, act), CVX_ERR_ALIGN,
+ * CVX_ERR_ALIAS, CVX_ERR_HIP.
+ */
+CVX_API cvx_status cvx_linear_grouped(const cvx_grouped_desc *d, const void *x, const float *x_scale,
+                                      const void *w, const float *scale, const float *bias,
+                                      const int *offset, const int *row_id, const float *row_weight,
+                                      void *y, void *stream);
+
 /* ------------------------------------------------------ placement report */
 /*
  * cvx_workgroup_xcds -- where a launch's workgroups run.  Launches n_workgroups

@@ -1,0 +1,358 @@
+"""cvx_linear_grouped against its definition in 64 bits, element by element.
+
+Tolerance.  Products of two 16-bit or two e4m3 values are exact in fp32, so a sum of K of
+them, in whatever order, is off by at most K*2^-24 of the sum of their magnitudes; where the
+e4m3 instructions align the products of eight consecutive channels to the largest of them, each of
+the other seven loses less than 2^-13 of that.  Sums of integers are exact, and rounded once.
+Scales, bias, the activation (whose slope is at most 1.1, and which is good to 8 units of fp32)
+and the row's factor take a dozen roundings of the magnitudes that meet there.  The output
+is rounded once, eps/2, or half the smallest subnormal."""
+import pytest
+import torch
+
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+from conv2d_batchnorm_activation_amd import cvx  # noqa: E402
+
+F16, BF16, E4M3, I8 = cvx.CVX_DT_F16, cvx.CVX_DT_BF16, cvx.CVX_DT_E4M3, cvx.CVX_DT_I8
+DT = {F16: torch.float16, BF16: torch.bfloat16, E4M3: torch.float8_e4m3fn, I8: torch.int8}
+U = 2.0 ** -24
+NONE, RELU, SILU = cvx.CVX_ACT_NONE, cvx.CVX_ACT_RELU, cvx.CVX_ACT_SILU
+
+
+def setup_module(module):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+class Case:
+    """Operands on the CPU, seeded; `run` puts them on the GPU, strided, and calls the library.
+
+    sizes: rows of each group; before, behind: rows outside of them; tokens: x's rows, found by
+    row_id (0: x by rows); bad: rows whose row_id names none."""
+
+    def __init__(self, seed, sizes, ci, co, dt=BF16, held=None, tokens=0, act=NONE, weight=False, scale=True, bias=True,
+                 before=0, behind=0, pads=(0, 0), bad=0):
+        g = torch.Generator().manual_seed(seed)
+        held = dt if held is None else held
+        self.sizes, self.ci, self.co, self.dt, self.held, self.act, self.pads = sizes, ci, co, dt, held, act, pads
+        self.n, self.rows = len(sizes), before + sum(sizes) + behind
+        self.offset = (before + torch.cat([torch.zeros(1), torch.tensor(sizes).cumsum(0)])).to(torch.int32)
+        rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        self.tokens = tokens or self.rows
+        x, w = rnd(self.tokens, ci), rnd(self.n, co, ci) / ci ** 0.5
+        self.sx = None
+        self.scale = 1 + 0.3 * rnd(self.n, co) if scale else None
+        self.bias = rnd(self.n, co) if bias else None
+        if held in (E4M3, I8):
+            self.sx = 0.01 + 0.02 * torch.rand(self.tokens, generator=g)
+            x, w = (x * 100, w * 40 * ci ** 0.5) if held == E4M3 else ((x * 40).round(), (w * 40 * ci ** 0.5).round())
+            top = 448 if held == E4M3 else 127
+            x, w = x.clamp(-top, top), w.clamp(-top, top)
+            self.scale = (self.scale if scale else torch.ones(self.n, co)) / 40 / ci ** 0.5
+        self.x, self.w = x.to(DT[held]), w.to(DT[held])
+        self.row_id = torch.randint(0, self.tokens, (self.rows,), generator=g).to(torch.int32) if tokens else None
+        if bad:
+            at = torch.randperm(self.rows, generator=g)[:bad]
+            self.row_id[at] = torch.tensor([-1, self.tokens, 2 ** 31 - 1, -2 ** 31])[torch.arange(bad) % 4].to(torch.int32)
+        self.weight = torch.rand(self.rows, generator=g) * 2 - 0.5 if weight else None
+
+    def desc(self):
+        px, py = self.pads
+        return cvx.make_grouped_desc(self.rows, self.tokens, self.n, self.ci, self.co, self.dt, self.held, self.act,
+                                     self.ci + px, self.co + py)
+
+    def upload(self):
+        px, py = self.pads
+        x = torch.zeros(self.tokens, self.ci + px, device=DEV)
+        x[:, self.ci:] = 100.0 if self.held == I8 else float("nan")
+        x = x.to(DT[self.held])
+        x[:, :self.ci] = self.x.to(DEV)
+        dev = lambda m: None if m is None else m.to(DEV)  # noqa: E731
+        self.ybuf = torch.full((self.rows + 2, self.co + py), 7.0, dtype=DT[self.dt], device=DEV)
+        return [self.desc(), x[:, :self.ci], dev(self.w), dev(self.offset), self.ybuf[1:-1, :self.co], dev(self.sx),
+                dev(self.scale), dev(self.bias), dev(self.row_id), dev(self.weight)]
+
+    def run(self, stream=None):
+        args = self.upload()
+        self.plan = cvx.cvx_linear_grouped_plan(args[0])
+        say(f"{self.plan} rows={self.rows} tokens={self.tokens} sizes={self.sizes[:20]} ci={self.ci} co={self.co} "
+            f"act={self.act} {self.pads}")
+        cvx.cvx_linear_grouped(*args, stream)
+        torch.cuda.synchronize()
+        b = self.ybuf.float().cpu()
+        assert (b[[0, -1]] == 7).all() and (b[:, self.co:] == 7).all(), "wrote outside the rows"
+        y = b[1:-1, :self.co].double()
+        a, e = int(self.offset[0]), int(self.offset[-1])
+        assert (y[:a] == 7).all() and (y[e:] == 7).all(), "wrote rows of no group"
+        return y[a:e]
+
+    def definition(self):
+        """(value, tolerance) of the groups' rows"""
+        f = torch.float64
+        ends = self.offset.tolist()
+        out, tols = [], []
+        fi = torch.finfo(DT[self.dt])
+        for d in range(self.n):
+            a, b = ends[d], ends[d + 1]
+            j = self.row_id[a:b].long() if self.row_id is not None else torch.arange(a, b)
+            live = (j >= 0) & (j < self.tokens)
+            j = torch.where(live, j, 0)
+            x, w = self.x[j].to(f) * live[:, None], self.w[d].to(f)
+            if self.sx is not None:
+                x = x * self.sx[j].to(f)[:, None]
+            if self.scale is not None:
+                w = w * self.scale[d].to(f)[:, None]
+            z, mag = x @ w.t(), x.abs() @ w.abs().t()
+            err = self.ci * U * mag if self.held != I8 else U * z.abs()
+            if self.held == E4M3 and "tile" in self.plan:
+                gx, gw = (m.abs().view(len(m), self.ci // 8, 8).amax(2) for m in (x, w))
+                err = err + 7 * 2.0 ** -13 * (gx @ gw.t())
+            if self.held == I8:
+                mag = z.abs()
+            if self.bias is not None:
+                z, mag = z + self.bias[d].to(f), mag + self.bias[d].to(f).abs()
+            z = z * torch.sigmoid(z) if self.act == SILU else torch.relu(z) if self.act == RELU else z
+            tol = 1.1 * (err + 14 * U * mag)
+            if self.weight is not None:
+                r = self.weight[a:b].to(f)[:, None]
+                z, tol = z * r, tol * r.abs() + U * (z * r).abs()
+            out.append(z)
+            tols.append(tol + (fi.eps / 2) * (z.abs() + tol) + fi.smallest_normal * fi.eps / 2)
+        return torch.cat(out), torch.cat(tols)
+
+
+def check(c):
+    got = c.run()
+    want, tol = c.definition()
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), f"{int(bad.sum())} out of bound, first at {bad.nonzero()[0].tolist()}: " \
+                          f"{got[bad][0].item()!r} for {want[bad][0].item()!r}"
+
+
+SHAPES = [
+    ([1], 8, 4, {}), ([1], 4096, 260, dict(act=SILU)), ([3, 0, 1], 144, 36, dict(act=RELU)),
+    ([0, 0, 5, 0], 272, 100, dict(behind=3)), ([1] * 9, 512, 516, dict(tokens=2)),
+    ([2, 1, 0, 4, 9, 1], 1008, 68, dict(tokens=5, weight=True)), ([16, 17, 15], 256, 132, dict(before=2, behind=1)),
+    ([33, 0, 64, 65, 1], 400, 64, dict(pads=(16, 4), act=SILU)), ([130], 64, 300, dict(tokens=40, bad=9)),
+    ([0, 200, 3, 0, 77], 1040, 516, dict(tokens=90, weight=True, act=SILU)), ([511, 2, 257], 144, 260, dict(scale=False)),
+    ([300, 0, 700, 129], 208, 1284, dict(bias=False, pads=(32, 8), behind=20)),
+    ([1200, 5, 0, 900], 528, 2052, dict(tokens=700, act=RELU)),
+]
+
+
+@pytest.mark.parametrize("sizes,ci,co,kw", SHAPES)
+@pytest.mark.parametrize("dt,held", [(BF16, BF16), (F16, F16), (BF16, E4M3), (F16, I8)])
+def test_groups(sizes, ci, co, kw, dt, held):
+    if held in (E4M3, I8) and ci % 16:
+        ci = 16
+    check(Case(len(sizes) * 31 + ci, sizes, ci, co, dt, held, **kw))
+
+
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 200, 1024])
+def test_many_groups(n):
+    g = torch.Generator().manual_seed(n)
+    sizes = (torch.rand(n, generator=g) ** 4 * 9).long().tolist()
+    sizes[-1] += 1
+    check(Case(n, sizes, 64, 20, tokens=50, behind=4))
+    check(Case(n, sizes, 64, 132, F16, I8, before=3, weight=True))
+
+
+def spread(seed, n, rows):
+    """Sizes of n groups, uneven, `rows` in all."""
+    g = torch.Generator().manual_seed(seed)
+    pick = torch.randn(rows, n, generator=g) + 1.5 * torch.randn(n, generator=g)
+    return torch.bincount(pick.argmax(1), minlength=n).tolist()
+
+
+@pytest.mark.parametrize("held", [BF16, E4M3, I8])
+@pytest.mark.parametrize("n,rows,ci,co", [(40, 60, 528, 388), (16, 150, 272, 1028), (8, 500, 144, 516), (6, 3000, 144, 1540)])
+def test_uneven_groups(n, rows, ci, co, held):
+    check(Case(rows, spread(n, n, rows), ci, co, BF16, held, tokens=rows // 2, weight=True, behind=7))
+
+
+def offsets(c, values):
+    """The case with these ends, and the groups that they mean."""
+    c.offset = torch.tensor(values, dtype=torch.int32)
+    args = c.upload()
+    say(f"ends {values}")
+    cvx.cvx_linear_grouped(*args)
+    torch.cuda.synchronize()
+    got = c.ybuf.float().cpu()
+    c.plan = cvx.cvx_linear_grouped_plan(args[0])
+    e = [min(max(v, 0), c.rows) for v in values]
+    for i in range(1, len(e)):
+        e[i] = max(e[i], e[i - 1])
+    c.offset = torch.tensor(e, dtype=torch.int32)
+    want, tol = c.definition()
+    assert ((got[1 + e[0]:1 + e[-1], :c.co].double() - want).abs() <= tol).all()
+    assert (got[:1 + e[0]] == 7).all() and (got[1 + e[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("values", [
+    [0, 10, 20, 30, 40], [5, 5, 5, 5, 5], [-9, 4, 90, 12, 13], [0, 30, 10, 20, 35], [2 ** 31 - 1] * 5, [-2 ** 31] * 5,
+    [40, 0, 0, 0, 0], [0, -5, 7, -2 ** 31, 2 ** 31 - 1], [3, 39, 2, 41, 0]])
+@pytest.mark.parametrize("held", [BF16, I8])
+def test_ends_of_any_kind(values, held):
+    offsets(Case(5, [10] * 4, 80, 36, BF16, held), values)
+
+
+def test_nothing_to_do():
+    c = Case(6, [0] * 70, 64, 36, behind=9)
+    got = c.run()
+    assert not got.numel()
+
+
+@pytest.mark.parametrize("sizes", [[3, 2, 4], [100, 60, 130], [600, 300, 600]])
+def test_infinities_and_nan_stay_with_their_group_and_row(sizes):
+    nan, inf = float("nan"), float("inf")
+    c = Case(8, sizes, 96, 516, act=RELU)
+    a, b = sizes[0], sizes[0] + sizes[1]
+    c.w[1, 3, 5], c.w[1, 4, 0] = nan, inf
+    c.x[0, 7] = nan
+    c.bias[2, 9] = inf
+    got = c.run()
+    assert torch.isnan(got[0]).all()
+    assert torch.isnan(got[a:b, 3]).all()
+    rest = torch.ones_like(got, dtype=torch.bool)
+    rest[0], rest[a:b, 3:5], rest[b:, 9] = False, False, False
+    assert torch.isfinite(got[rest]).all() and (got[b:, 9] == inf).all()
+
+
+def test_the_same_row_many_times_and_shared_buffers():
+    # every row of y the same row of x: as the projection of one token by each group
+    c = Case(9, [40, 3, 90], 272, 132, tokens=3)
+    c.row_id.fill_(1)
+    got = c.run()
+    for a, b in ((0, 40), (40, 43), (43, 133)):
+        assert (got[a:b] == got[a]).all()
+    check(c)
+
+
+@pytest.mark.parametrize("held", [BF16, E4M3, I8])
+def test_like_the_projection(held):
+    # one group of all rows is the projection
+    c = Case(10, [700], 1040, 2052, BF16, held)
+    got = c.run()
+    y = torch.empty(700, 2052, dtype=torch.bfloat16, device=DEV)
+    cvx.cvx_linear(cvx.make_linear_desc(700, 1040, 2052, BF16, held), c.x.to(DEV), c.w[0].to(DEV), y,
+                   None if c.sx is None else c.sx.to(DEV), c.scale[0].to(DEV), c.bias[0].to(DEV))
+    want, tol = c.definition()
+    assert ((y.cpu().double() - got).abs() <= 2 * tol).all()
+
+
+def test_far_weights_and_rows():
+    # 5 GB of weights, the last group's past 32-bit offsets; rows of x and y spread over 4.6 GB
+    n, ci, co = 9, 8192, 34000
+    w = torch.zeros(n, co, ci, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    w[-1, -300:] = torch.randn(300, ci, generator=g, device=DEV).to(torch.bfloat16) / 90
+    for rows in (3, 200):
+        x = torch.randn(rows, ci, generator=g, device=DEV).to(torch.bfloat16)
+        y = torch.empty(rows, co, dtype=torch.bfloat16, device=DEV)
+        offset = torch.tensor([0] * n + [rows], dtype=torch.int32, device=DEV)
+        say(f"groups with 5 GB of weights, {rows} rows")
+        cvx.cvx_linear_grouped(cvx.make_grouped_desc(rows, rows, n, ci, co, BF16), x, w, offset, y)
+        xd, wd = x.cpu().double(), w[-1, -300:].cpu().double()
+        want = xd @ wd.t()
+        tol = ci * U * (xd.abs() @ wd.abs().t()) + 2.0 ** -8 * want.abs() + 1e-30
+        assert ((y[:, -300:].cpu().double() - want).abs() <= tol).all() and not y[:, :1000].any()
+    del w, x, y
+    t, wide = 1100, 1 << 21
+    c = Case(5, [300, 20, 0, 780], 80, 68)
+    big = [torch.zeros(t * wide, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    x, y = (torch.as_strided(b, (t, k), (wide, 1)) for b, k in zip(big, (c.ci, c.co)))
+    x.copy_(c.x.to(DEV))
+    d = cvx.make_grouped_desc(t, t, 4, c.ci, c.co, BF16, x_stride=wide, y_stride=wide)
+    c.plan = cvx.cvx_linear_grouped_plan(d)
+    say("groups of far rows")
+    cvx.cvx_linear_grouped(d, x, c.w.to(DEV), c.offset.to(DEV), y, None, c.scale.to(DEV), c.bias.to(DEV))
+    want, tol = c.definition()
+    assert ((y.cpu().double() - want).abs() <= tol).all()
+
+
+class Experts:
+    """A layer's experts as they are used: rows by expert, first product, gate, second product with the
+    router's factors, the sum of a token's rows."""
+
+    def __init__(self, t, top, n, c, inner, held, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        self.t, self.top, self.n, self.c, self.inner, self.held = t, top, n, c, inner, held
+        rows = t * top
+        expert, order = torch.randn(t, n, generator=g).topk(top, 1)[1].reshape(-1).sort(stable=True)
+        sizes = torch.bincount(expert, minlength=n).tolist()
+        self.one = Case(seed + 1, sizes, c, 2 * inner, BF16, held, tokens=t)
+        self.two = Case(seed + 2, sizes, inner, c, BF16, held, weight=True)
+        self.one.row_id = (order // top).to(torch.int32)
+        self.place = torch.empty(rows, dtype=torch.long)
+        self.place[order] = torch.arange(rows)
+        self.args = [self.one.upload(), self.two.upload()]
+        self.h = self.one.ybuf[1:-1]
+        self.a, self.q = self.args[1][1], self.args[1][5]
+        self.gd = cvx.make_gate_desc(rows, inner, BF16, held, cvx.CVX_ACT_SILU, 2 * inner, 2 * inner)
+        self.at = self.place.to(DEV)
+
+    def run(self, stream=None):
+        cvx.cvx_linear_grouped(*self.args[0], stream)
+        cvx.cvx_gate(self.gd, self.h[:, :self.inner], self.h[:, self.inner:], self.a, self.q, stream)
+        cvx.cvx_linear_grouped(*self.args[1], stream)
+
+    def results(self):
+        y = self.two.ybuf[1:-1]
+        return [self.h.clone(), self.a.view(torch.uint8).clone(), y.clone(), y[self.at].view(self.t, self.top, -1).float().sum(1)]
+
+
+@pytest.mark.parametrize("held", [BF16, E4M3, I8])
+@pytest.mark.parametrize("t", [1, 9, 150])
+def test_experts_of_a_layer(t, held):
+    L = Experts(t, 3, 7, 272, 144, held, t)
+    say(f"experts of a layer, {t} tokens, held={held}")
+    L.run()
+    torch.cuda.synchronize()
+    first = L.results()
+    L.one.plan, L.two.plan = (cvx.cvx_linear_grouped_plan(c.desc()) for c in (L.one, L.two))
+    want, tol = L.one.definition()
+    assert ((first[0].cpu().double() - want).abs() <= tol).all()
+    L.two.x, L.two.sx = L.a.cpu(), None if L.q is None else L.q.cpu()
+    want, tol = L.two.definition()
+    assert ((first[2].cpu().double() - want).abs() <= tol).all()
+    total = want[L.place].view(t, 3, -1).sum(1)
+    assert ((first[3].cpu().double() - total).abs() <= tol[L.place].view(t, 3, -1).sum(1) + 4 * U * first[2].abs().max().item()).all()
+    # in a graph, over other inputs, with eager work between the replays
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        L.run()
+    x = L.args[0][1].view(torch.uint8)
+    keep, other = x.clone(), x.flip(0).contiguous()
+    for i in range(4):
+        x.copy_(other if i % 2 == 0 else keep)
+        for m in (L.one.ybuf, L.two.ybuf, L.a):
+            m.view(torch.uint8).fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = L.results()
+        L.run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, L.results()))
+    assert torch.equal(got[2], first[2])
+
+
+def test_on_streams_of_their_own():
+    layers = [Experts(t, 2, 6, 272, 144, h, 40 + t) for t, h in ((5, BF16), (90, I8), (400, E4M3))]
+    want = []
+    for L in layers:
+        L.run()
+        torch.cuda.synchronize()
+        want.append(L.results())
+    streams = [torch.cuda.Stream() for _ in layers]
+    say("experts on streams of their own")
+    for _ in range(5):
+        for L, s in zip(layers, streams):
+            L.run(s)
+    torch.cuda.synchronize()
+    for L, w in zip(layers, want):
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(L.results(), w))
