@@ -4,8 +4,10 @@
 // The products are those of k_linear_tile.hip (weights the A operand, rows the B
 // operand, lin_tile.h has the loop).  How many rows a group has stands in device
 // memory, so the tiles are counted there: a workgroup stays for several tiles, begins
-// with a scan of the groups' ends, and finds a tile's group by its number.  Rows are
-// read where they lie (row_id), so that tokens need no copy in the groups' order.
+// with a scan of the groups' ends, and finds a tile's group by its number.  The first
+// stages of its next tile arrive while a tile finishes.  A group's last tile, where it has half of the rows or fewer, takes half
+// of the products.  Rows are read where they lie (row_id), so that tokens need no copy
+// in the groups' order.
 #include <stdio.h>
 
 #include "cvx_internal.h"
@@ -68,6 +70,17 @@ __device__ __forceinline__ int group_of(const GroupArgs& a, int lane, const Grou
     return n - 1;
 }
 
+// A tile: its group, its first channel, its first row and how many rows; of none, 0.
+struct Where {
+    int g, m0, n0, nrows;
+};
+
+// 64 values of four bytes into LDS, lane l's from byte `off` of the operand.
+__device__ __forceinline__ void fetch64(rsrc_t r, unsigned off, void* to)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, (int)off, 0, 0, 0);
+}
+
 // WM x WN waves, each MB x NB blocks of 32 x 32; D stage buffers.
 template <typename T, int X, int WM, int WN, int MB, int NB, int D>
 __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_grouped(GroupArgs a)
@@ -76,12 +89,14 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_grouped
     typedef typename tile::v4 v4;
     constexpr bool Q = X != kX16;  // 8-bit operands, tokens' scales
     constexpr unsigned XB = tile::XB;
-    constexpr int NT = tile::NT, BM = tile::BM, BN = tile::BN, SB = tile::SB;
+    constexpr int W = tile::W, NT = tile::NT, BM = tile::BM, BN = tile::BN, SB = tile::SB;
+    constexpr int TOK = 16;  // rows that are turned at a time
     // an array a stage, so that waits are for the stage read, not for every fetch
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[SB], buf1[SB], buf2[D == 4 ? SB : 16],
         buf3[D == 4 ? SB : 16];
+    __shared__ __attribute__((aligned(16))) unsigned char turn[W * 128 * TOK];
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
-    __shared__ float sx_lds[Q ? BN : 1], rw_lds[BN];
+    __shared__ float sx_lds[2][Q ? BN : 64], rw_lds[BN];  // (x's scales of this tile and the next)
     __shared__ Groups groups;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -90,97 +105,163 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_grouped
     const unsigned cb = (unsigned)a.cin * XB, pitch = (unsigned)a.xs * XB;
 
     if (wave == 0) count_tiles<BN>(a, lane, groups);
+    // what is not given stays as it is set here
+    for (int i = tid; i < BM; i += NT) {
+        sc_lds[i] = 1.0f;
+        bi_lds[i] = 0.0f;
+    }
+    for (int i = tid; i < BN; i += NT) rw_lds[i] = 1.0f;
     __syncthreads();
     // Workgroups go to the XCDs in turn: each XCD has a run of the tiles, which its
     // workgroups take in turn.
-    const int n = a.tiles_m * groups.first[a.groups];
+    const int n = a.tiles_m * __builtin_amdgcn_readfirstlane(groups.first[a.groups]);
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
     const int per = n >> 3, rest = n & 7;
     const int lo = xcd * per + (xcd < rest ? xcd : rest), up = lo + per + (xcd < rest ? 1 : 0);
-    for (int at = lo + (int)(blockIdx.x >> 3); at < up; at += step) {
-        // of a group, eight tiles of channels go before the next tile of rows
-        const int g = __builtin_amdgcn_readfirstlane(group_of(a, lane, groups, a.tiles_m, at));
-        const int tn = groups.first[g + 1] - groups.first[g], in = at - groups.first[g] * a.tiles_m;
-        const int wide = 8 * tn, run = in / wide, ir = in - run * wide;
-        const int gm = a.tiles_m - 8 * run < 8 ? a.tiles_m - 8 * run : 8;
-        const int tr = ir / gm;
-        const int m0 = (8 * run + ir - tr * gm) * BM;
-        const int n0 = __builtin_amdgcn_readfirstlane(groups.start[g] + tr * BN);
-        const int left = __builtin_amdgcn_readfirstlane(groups.start[g + 1]) - n0;
-        const int nrows = left < BN ? left : BN;
-        const int mrows = a.cout - m0 < BM ? a.cout - m0 : BM;
+    auto find = [&](int at) {
+        Where t = {0, 0, 0, 0};
+        if (at >= up) return t;
+        // Of a group, four tiles of rows go with a tile of channels before the next of these,
+        // so that tiles which share weights are taken at the same time.  (The numbers are the
+        // same in all lanes, which the compiler is told where it does not see it.)
+        auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        t.g = same(group_of(a, lane, groups, a.tiles_m, at));
+        const int first = same(groups.first[t.g]), start = same(groups.start[t.g]);
+        const int tn = same(groups.first[t.g + 1]) - first, in = at - first * a.tiles_m;
+        const int run = same(in / (4 * a.tiles_m)), ir = in - run * 4 * a.tiles_m;
+        const int gn = tn - 4 * run < 4 ? tn - 4 * run : 4;
+        const int tm = same(ir / gn);
+        t.m0 = tm * BM;
+        t.n0 = start + (4 * run + ir - tm * gn) * BN;
+        const int left = same(groups.start[t.g + 1]) - t.n0;
+        t.nrows = left < BN ? left : BN;
+        return t;
+    };
+    // the row of x that row r of a tile is (not below a.tokens where there is none)
+    auto source = [&](const Where& t, int r) {
+        if (r >= t.nrows) return 0x7fffffff;
+        return a.row_id ? a.row_id[t.n0 + r] : t.n0 + r;
+    };
+    // this lane's fetches of x, and where it fetches x's scales, the rows these are of
+    constexpr int FN = tile::FN, FS = Q ? (BN / 64 + W - 1) / W : 1;
+    struct Sources {
+        int x[FN], sx[FS];
+    };
+    auto sources = [&](const Where& t) {
+        Sources s;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) s.x[i] = source(t, tile::fetch_row(wave, lane, i));
+#pragma unroll
+        for (int i = 0; i < FS; ++i) s.sx[i] = Q ? source(t, 64 * (wave + W * i) + lane) : 0;
+        return s;
+    };
+    // a tile's operands, with the fetch of x's scales begun
+    auto operands = [&](const Where& t, const Sources& s, float* sx) {
         TileRows op;
-        op.w = static_cast<const char*>(a.w) + ((long)g * a.cout + m0) * cb;
-        op.wend = (unsigned)mrows * cb;
+        op.w = static_cast<const char*>(a.w) + ((long)t.g * a.cout + t.m0) * cb;
+        op.wend = (unsigned)(a.cout - t.m0 < BM ? a.cout - t.m0 : BM) * cb;
+        op.x = static_cast<const char*>(a.x) + (a.row_id ? 0l : (long)t.n0 * pitch);
+        op.xend = (unsigned)((a.row_id ? a.tokens : t.nrows) - 1) * pitch + cb;
 #pragma unroll
         for (int i = 0; i < tile::FM; ++i)
             op.wo[i] = (unsigned)tile::fetch_row(wave, lane, i) * cb + tile::piece(wave, lane);
-        // the row of x that a row of the tile is, or -1
-        auto source = [&](int r) {
-            if (r >= nrows) return -1;
-            const int j = a.row_id ? a.row_id[n0 + r] : n0 + r;
-            return j < a.tokens ? j : -1;
-        };
-        op.x = static_cast<const char*>(a.x) + (a.row_id ? 0l : (long)n0 * pitch);
-        op.xend = (unsigned)((a.row_id ? a.tokens : nrows) - 1) * pitch + cb;
 #pragma unroll
-        for (int i = 0; i < tile::FN; ++i) {
-            const int r = tile::fetch_row(wave, lane, i), j = source(r);
-            op.xo[i] = j < 0 ? kOOB : (unsigned)(a.row_id ? j : r) * pitch + tile::piece(wave, lane);
-        }
-        for (int i = tid; i < BM; i += NT) {
-            const bool ok = m0 + i < a.cout;
-            sc_lds[i] = !a.scale ? 1.0f : ok ? a.scale[(long)g * a.cout + m0 + i] : 0.0f;
-            bi_lds[i] = a.bias && ok ? a.bias[(long)g * a.cout + m0 + i] : 0.0f;
-        }
-        for (int i = tid; i < BN; i += NT) {
-            if constexpr (Q) {
-                const int j = source(i);
-                sx_lds[i] = j < 0 ? 0.0f : a.x_scale[j];
-            }
-            rw_lds[i] = a.weight && i < nrows ? a.weight[n0 + i] : 1.0f;
-        }
-        typename tile::sum_t total[MB][NB];
-        tile::sums(op, cb, wave, lane, buf0, buf1, buf2, buf3, total);
+        for (int i = 0; i < FN; ++i)
+            op.xo[i] = (unsigned)s.x[i] >= (unsigned)a.tokens
+                           ? kOOB
+                           : (unsigned)(s.x[i] - (a.row_id ? 0 : t.n0)) * pitch + tile::piece(wave, lane);
+        if constexpr (Q)
+#pragma unroll
+            for (int i = 0; i < FS; ++i)
+                if (64 * (wave + W * i) < BN)
+                    fetch64(make_rsrc(a.x_scale, 4u * (unsigned)a.tokens),
+                            (unsigned)s.sx[i] >= (unsigned)a.tokens ? kOOB : 4u * (unsigned)s.sx[i],
+                            sx + 64 * (wave + W * i));
+        return op;
+    };
 
-        // as in k_linear_tile.hip: lane (hi, l32) holds channels 8j + 4hi + 0..3 of one row
-        v4 out[NB][MB][4];
+    int at = lo + (int)(blockIdx.x >> 3);
+    if (at >= up) return;
+    Where cur = find(at);
+    float *sx0 = sx_lds[0], *sx1 = sx_lds[1];
+    TileRows op = operands(cur, sources(cur), sx0);
+    tile::begin(op, cb, wave, lane, buf0, buf1, buf2, buf3);
+    for (;;) {
+        // What the end needs comes into LDS under the products: no wave reads the tile
+        // before any more.  (It is there when the first stages' barriers are passed.)
+        const int mrows = a.cout - cur.m0 < BM ? a.cout - cur.m0 : BM;
+        for (int i = wave; i < BM / 64; i += W) {
+            const unsigned off = 4u * (unsigned)(64 * i + lane), end = 4u * (unsigned)mrows;
+            const long from = (long)cur.g * a.cout + cur.m0;
+            if (a.scale) fetch64(make_rsrc(a.scale + from, end), off, sc_lds + 64 * i);
+            if (a.bias) fetch64(make_rsrc(a.bias + from, end), off, bi_lds + 64 * i);
+        }
+        if (a.weight)
+            for (int i = wave; i < BN / 64; i += W)
+                fetch64(make_rsrc(a.weight + cur.n0, 4u * (unsigned)cur.nrows), 4u * (unsigned)(64 * i + lane),
+                        rw_lds + 64 * i);
+        at += step;
+        const Where nxt = find(at);
+        const Sources far = sources(nxt);  // (arrives under the products)
+
+        // NL blocks of 32 rows a wave: half of them where they hold the tile's rows
+        auto work = [&](auto blocks) {
+            constexpr int NL = decltype(blocks)::value;
+            typename tile::sum_t total[MB][NL];
+            tile::template sums<true, NL>(op, cb, wave, lane, buf0, buf1, buf2, buf3, total);
+            if (nxt.nrows) {
+                op = operands(nxt, far, sx1);
+                tile::begin(op, cb, wave, lane, buf0, buf1, buf2, buf3);
+            }
+
+            // as in k_linear_tile.hip: lane (hi, l32) holds channels 8j + 4hi + 0..3 of one row
+            v4 out[NL][MB][4];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int t = (wn * NB + n) * 32 + l32;
-            const float sx = Q ? sx_lds[t] : 1.0f, rw = rw_lds[t];
-            f32x16 acc[MB];
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = (wm * MB + m) * 32 + 8 * j + 4 * hi;
-                    const f32x4 sc = *reinterpret_cast<const f32x4*>(sc_lds + c);
-                    const f32x4 bi = *reinterpret_cast<const f32x4*>(bi_lds + c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float z = (float)total[m][n][4 * j + i];  // of integers: rounded once from 2^24 up
-                        acc[m][4 * j + i] = fmaf(Q ? z * sx : z, sc[i], bi[i]);
-                    }
-                }
-            auto activate = [&](auto act) {
+            for (int n = 0; n < NL; ++n) {
+                const int t = (wn * NL + n) * 32 + l32;
+                const float sx = Q ? sx0[t] : 1.0f, rw = rw_lds[t];
+                f32x16 acc[MB];
 #pragma unroll
                 for (int m = 0; m < MB; ++m)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[m][i] = apply_act_nan(acc[m][i], decltype(act)::value);
-            };
-            if (a.act == CVX_ACT_RELU) activate(std::integral_constant<int, CVX_ACT_RELU>());
-            if (a.act == CVX_ACT_SILU) activate(std::integral_constant<int, CVX_ACT_SILU>());
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = (wm * MB + m) * 32 + 8 * j + 4 * hi;
+                        const f32x4 sc = *reinterpret_cast<const f32x4*>(sc_lds + c);
+                        const f32x4 bi = *reinterpret_cast<const f32x4*>(bi_lds + c);
 #pragma unroll
-            for (int m = 0; m < MB; ++m)
+                        for (int i = 0; i < 4; ++i) {
+                            const float z = (float)total[m][n][4 * j + i];  // of integers: rounded once from 2^24 up
+                            acc[m][4 * j + i] = fmaf(Q ? z * sx : z, sc[i], bi[i]);
+                        }
+                    }
+                auto activate = [&](auto act) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) out[n][m][i / 4][i % 4] = (T)(acc[m][i] * rw);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        const rsrc_t ry =
-            make_rsrc(static_cast<T*>(a.y) + (long)n0 * a.ys, (unsigned)((nrows - 1) * a.ys + a.cout) * 2u);
-        tile::store(out, buf0, wave, lane, ry, nrows, (unsigned)a.ys, m0, a.cout);
-        lds_barrier();  // LDS is free for the next tile
+                    for (int m = 0; m < MB; ++m)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[m][i] = apply_act_nan(acc[m][i], decltype(act)::value);
+                };
+                if (a.act == CVX_ACT_RELU) activate(std::integral_constant<int, CVX_ACT_RELU>());
+                if (a.act == CVX_ACT_SILU) activate(std::integral_constant<int, CVX_ACT_SILU>());
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) out[n][m][i / 4][i % 4] = (T)(acc[m][i] * rw);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const rsrc_t ry =
+                make_rsrc(static_cast<T*>(a.y) + (long)cur.n0 * a.ys, (unsigned)((cur.nrows - 1) * a.ys + a.cout) * 2u);
+            tile::template store<NL, TOK>(out, turn, wave, lane, ry, cur.nrows, (unsigned)a.ys, cur.m0, a.cout);
+        };
+        if (NB == 1 || cur.nrows > BN / 2)
+            work(std::integral_constant<int, NB>());
+        else if constexpr (NB > 1)
+            work(std::integral_constant<int, NB / 2>());
+        if (nxt.nrows == 0) break;
+        lds_barrier();  // no wave reads this tile's operands of the end any more
+        cur = nxt;
+        float* const used = sx0;
+        sx0 = sx1;
+        sx1 = used;
     }
 }
 

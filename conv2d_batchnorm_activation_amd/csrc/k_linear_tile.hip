@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         if (LORA) id_lds[i] = adapter_of(a, token);
     }
     typename tile::sum_t total[MB][NB];
-    tile::sums(op, cb, wave, lane, buf0, buf1, buf2, buf3, total);
+    tile::template sums<false, NB>(op, cb, wave, lane, buf0, buf1, buf2, buf3, total);
 
     // 32 tokens at a time; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one
     // token.  A load waits for the stores before it, so finished values are kept,
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    tile::store(out, buf0, wave, lane, ry, nrows, (unsigned)a.ys, m0, a.cout);
+    tile::template store<NB, 32>(out, buf0, wave, lane, ry, nrows, (unsigned)a.ys, m0, a.cout);
 }
 
 template <typename T, int X, int WM, int WN, int MB, int NB, int D>

@@ -61,37 +61,56 @@ struct Tile {
     // The row of the tile that this lane's part of fetch i is of.
     static __device__ __forceinline__ int fetch_row(int wave, int lane, int i) { return 8 * (wave + W * i) + (lane >> 3); }
 
-    // The sums over all stages of rows of cb bytes.  All waves of the workgroup call
-    // it; nothing is under way in LDS before, and nothing after.
-    static __device__ __forceinline__ void sums(const TileRows& o, unsigned cb, int wave, int lane, unsigned char* buf0,
-                                                unsigned char* buf1, unsigned char* buf2, unsigned char* buf3,
-                                                sum_t (&acc)[MB][NB])
+    // The fetches of stage `st` of a tile into a stage buffer.
+    static __device__ __forceinline__ void issue(const TileRows& o, unsigned cb, int st, unsigned char* buf, int wave,
+                                                 int lane)
+    {
+        const unsigned pc = piece(wave, lane);
+        const unsigned kb = (unsigned)st * 128 < cb ? (unsigned)st * 128 : 0u;  // past the end: nothing is live
+        const unsigned dead = (unsigned)st * 128 + pc < cb ? 0u : kOOB;
+        const char *wk = o.w + kb, *xk = o.x + kb;
+        const unsigned wleft = o.wend - kb, xleft = o.xend - kb;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wk, wleft), (lds_void*)(buf + 1024 * (wave + W * i)), 16,
+                                                     o.wo[i] | dead, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xk, xleft),
+                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16,
+                                                     o.xo[i] | dead, 0, 0, 0);
+    }
+    // The first D stages.
+    static __device__ __forceinline__ void begin(const TileRows& o, unsigned cb, int wave, int lane, unsigned char* buf0,
+                                                 unsigned char* buf1, unsigned char* buf2, unsigned char* buf3)
+    {
+        issue(o, cb, 0, buf0, wave, lane);
+        issue(o, cb, 1, buf1, wave, lane);
+        if constexpr (D == 4) {
+            issue(o, cb, 2, buf2, wave, lane);
+            issue(o, cb, 3, buf3, wave, lane);
+        }
+    }
+
+    // The sums over all stages of rows of cb bytes, of the first 32*WN*NL rows of the
+    // tile (wave wn takes NL blocks of them).  All waves of the workgroup call it.
+    // BEGUN: the tile's first D stages are under way.  Else nothing is under way in LDS
+    // before it, and after it nothing in either case.
+    template <bool BEGUN, int NL>
+    static __device__ __forceinline__ void sums(const TileRows& o, unsigned cb, int wave, int lane,
+                                                unsigned char* buf0, unsigned char* buf1, unsigned char* buf2,
+                                                unsigned char* buf3, sum_t (&acc)[MB][NL])
     {
         const int wm = wave % WM, wn = wave / WM;
         const int hi = lane >> 5, l32 = lane & 31;
         const int nst = (int)((cb + 127) / 128);
-        const unsigned pc = piece(wave, lane);
-        auto issue = [&](int st, unsigned char* buf) {
-            const unsigned kb = (unsigned)st * 128 < cb ? (unsigned)st * 128 : 0u;  // past the end: nothing is live
-            const unsigned dead = (unsigned)st * 128 + pc < cb ? 0u : kOOB;
-            const char *wk = o.w + kb, *xk = o.x + kb;
-            const unsigned wleft = o.wend - kb, xleft = o.xend - kb;
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wk, wleft), (lds_void*)(buf + 1024 * (wave + W * i)), 16,
-                                                         o.wo[i] | dead, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xk, xleft),
-                                                         (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16,
-                                                         o.xo[i] | dead, 0, 0, 0);
-        };
+        auto issue = [&](int st, unsigned char* buf) { Tile::issue(o, cb, st, buf, wave, lane); };
         unsigned slot[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) slot[s] = (unsigned)(l32 * 128 + (((2 * s + hi) ^ ((l32 >> 1) & 7)) * 16));
-        auto read = [&](const unsigned char* buf, int st, op_t(&A)[MB], op_t(&B)[NB]) {
+        auto read = [&](const unsigned char* buf, int st, op_t(&A)[MB], op_t(&B)[NL]) {
             const unsigned char* pa = buf + wm * MB * 4096;
-            const unsigned char* pb = buf + BM * 128 + wn * NB * 4096;
+            const unsigned char* pb = buf + BM * 128 + wn * NL * 4096;
             auto one = [&](const unsigned char* p) {
                 if constexpr (X8) {
                     const u32x4 x = *reinterpret_cast<const u32x4*>(p + slot[2 * st]);
@@ -108,7 +127,7 @@ struct Tile {
                 }
             };
 #pragma unroll
-            for (int n = 0; n < NB; ++n) B[n] = one(pb + 4096 * n);
+            for (int n = 0; n < NL; ++n) B[n] = one(pb + 4096 * n);
 #pragma unroll
             for (int m = 0; m < MB; ++m) A[m] = one(pa + 4096 * m);
         };
@@ -116,14 +135,14 @@ struct Tile {
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NL; ++n)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0;
-        auto mul = [&](const op_t(&A)[MB], const op_t(&B)[NB]) {
+        auto mul = [&](const op_t(&A)[MB], const op_t(&B)[NL]) {
 #pragma unroll
             for (int m = 0; m < MB; ++m)
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
+                for (int n = 0; n < NL; ++n) {
                     if constexpr (X8)
                         acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A[m], B[n], acc[m][n], 0, 0, 0,
                                                                                     0x7f7f7f7f, 0, 0x7f7f7f7f);
@@ -136,7 +155,7 @@ struct Tile {
         // Orders a step's instructions: the reads of the next operands and the fetches
         // of a later stage between the matrix instructions.
         auto mix = [&](auto fetches) {
-            constexpr int READS = (X8 ? 2 : 1) * (MB + NB), MUL = MB * NB, F = decltype(fetches)::value;
+            constexpr int READS = (X8 ? 2 : 1) * (MB + NL), MUL = MB * NL, F = decltype(fetches)::value;
             constexpr int OTHER = READS + F;
 #pragma unroll
             for (int i = 0; i < MUL; ++i) {
@@ -151,7 +170,7 @@ struct Tile {
             }
         };
         auto mix_all = [&]() {  // the same for a whole stage
-            constexpr int READS = (X8 ? 2 : 1) * (MB + NB) * STEPS, MUL = MB * NB * STEPS, OTHER = READS + FM + FN;
+            constexpr int READS = (X8 ? 2 : 1) * (MB + NL) * STEPS, MUL = MB * NL * STEPS, OTHER = READS + FM + FN;
 #pragma unroll
             for (int i = 0; i < MUL; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
@@ -164,12 +183,12 @@ struct Tile {
                 }
             }
         };
-        // Both loops take D stages; those past the last are zeros, and so are the fetches past it.
         typedef std::integral_constant<int, FM + FN> fetch;
         if constexpr (D == 2) {
-            // A step's operands are read under the step before.
+            // A step's operands are read under the step before.  Both loops take D stages;
+            // those past the last are zeros, and so are the fetches past it.
             typedef std::integral_constant<int, 0> no_fetch;
-            op_t A0[MB], B0[NB], A1[MB], B1[NB];
+            op_t A0[MB], B0[NL], A1[MB], B1[NL];
             auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
 #pragma unroll
                 for (int s = 0; s + 1 < STEPS; ++s) {
@@ -189,10 +208,15 @@ struct Tile {
                 mul(A1, B1);
                 mix(fetch());
             };
-            issue(0, buf0);
-            wait_arrived<0>();
-            stage_barrier();
-            issue(1, buf1);
+            if constexpr (BEGUN) {
+                wait_arrived<FM + FN>();
+                stage_barrier();
+            } else {
+                issue(0, buf0);
+                wait_arrived<0>();
+                stage_barrier();
+                issue(1, buf1);
+            }
             read(buf0, 0, A0, B0);
             for (int st = 0; st < nst; st += 2) {
                 stage(st, buf0, buf1);
@@ -201,13 +225,13 @@ struct Tile {
         } else {
             // One wave a SIMD: a stage's operands are all read under the stage before, as
             // a step's products (four instructions) are shorter than a read takes.
-            op_t A0[STEPS][MB], B0[STEPS][NB], A1[STEPS][MB], B1[STEPS][NB];
-            auto read_all = [&](const unsigned char* buf, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB]) {
+            op_t A0[STEPS][MB], B0[STEPS][NL], A1[STEPS][MB], B1[STEPS][NL];
+            auto read_all = [&](const unsigned char* buf, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NL]) {
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) read(buf, s, A[s], B[s]);
             };
-            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NB],
-                             op_t(&An)[STEPS][MB], op_t(&Bn)[STEPS][NB]) {
+            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NL],
+                             op_t(&An)[STEPS][MB], op_t(&Bn)[STEPS][NL]) {
                 wait_arrived<2 * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
                 stage_barrier();
                 issue(st + 4, cur);
@@ -216,10 +240,12 @@ struct Tile {
                 for (int s = 0; s < STEPS; ++s) mul(A[s], B[s]);
                 mix_all();
             };
-            issue(0, buf0);
-            issue(1, buf1);
-            issue(2, buf2);
-            issue(3, buf3);
+            if constexpr (!BEGUN) {
+                issue(0, buf0);
+                issue(1, buf1);
+                issue(2, buf2);
+                issue(3, buf3);
+            }
             wait_arrived<3 * (FM + FN)>();
             stage_barrier();
             read_all(buf0, A0, B0);
@@ -235,37 +261,44 @@ struct Tile {
     }
 
     // Writes finished values, `out`[n][m] a lane's sixteen channels of a token, four at a
-    // time: they are turned in LDS (4 KB a wave from `room`), so that a store takes whole
-    // lines.  ry: the rows from the tile's first token; m0: its first channel.
-    static __device__ __forceinline__ void store(const v4 (&out)[NB][MB][4], unsigned char* room, int wave, int lane,
+    // time: they are turned in LDS, TOK tokens (32 or 16) and 128*TOK bytes of `room` a
+    // wave at a time, so that a store takes whole lines.  ry: the rows from the tile's
+    // first token; m0: its first channel.
+    template <int NL, int TOK>
+    static __device__ __forceinline__ void store(const v4 (&out)[NL][MB][4], unsigned char* room, int wave, int lane,
                                                  rsrc_t ry, int nrows, unsigned ys, int m0, int cout)
     {
         const int wm = wave % WM, wn = wave / WM;
         const int hi = lane >> 5, l32 = lane & 31;
-        unsigned char* turn = room + wave * 4096;
+        unsigned char* turn = room + wave * 128 * TOK;
         const int p = lane & 7;
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NL; ++n)
 #pragma unroll
-            for (int m = 0; m < MB; m += 2) {
+            for (int m = 0; m < MB; m += 2)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<v4*>(turn + l32 * 128 + ((k ^ (l32 & 7)) * 16) + 8 * hi) = out[n][m + k / 4][k % 4];
-                wave_lds_order();
-                const int c = m0 + (wm * MB + m) * 32 + 8 * p;
+                for (int part = 0; part < 32 / TOK; ++part) {
+                    if (TOK == 32 || l32 / TOK == part) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tt = 8 * i + (lane >> 3), t = (wn * NB + n) * 32 + tt;
-                    const u32x4 q = *reinterpret_cast<const u32x4*>(turn + tt * 128 + ((p ^ (tt & 7)) * 16));
-                    const unsigned off = ((unsigned)t * ys + (unsigned)c) * 2u;
-                    const bool live = t < nrows;
-                    __builtin_amdgcn_raw_buffer_store_b128(q, ry, live && c + 8 <= cout ? (int)off : (int)kOOB, 0, 0);
-                    if (cout & 4)  // the last four channels of a row
-                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{q[0], q[1]}, ry,
-                                                              live && c + 4 == cout ? (int)off : (int)kOOB, 0, 0);
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<v4*>(turn + l32 % TOK * 128 + ((k ^ (l32 & 7)) * 16) + 8 * hi) =
+                                out[n][m + k / 4][k % 4];
+                    }
+                    wave_lds_order();
+                    const int c = m0 + (wm * MB + m) * 32 + 8 * p;
+#pragma unroll
+                    for (int i = 0; i < TOK / 8; ++i) {
+                        const int tt = 8 * i + (lane >> 3), t = (wn * NL + n) * 32 + TOK * part + tt;
+                        const u32x4 q = *reinterpret_cast<const u32x4*>(turn + tt * 128 + ((p ^ (tt & 7)) * 16));
+                        const unsigned off = ((unsigned)t * ys + (unsigned)c) * 2u;
+                        const bool live = t < nrows;
+                        __builtin_amdgcn_raw_buffer_store_b128(q, ry, live && c + 8 <= cout ? (int)off : (int)kOOB, 0, 0);
+                        if (cout & 4)  // the last four channels of a row
+                            __builtin_amdgcn_raw_buffer_store_b64(u32x2{q[0], q[1]}, ry,
+                                                                  live && c + 4 == cout ? (int)off : (int)kOOB, 0, 0);
+                    }
+                    wave_lds_order();
                 }
-                wave_lds_order();
-            }
     }
 };
 
