@@ -101,7 +101,7 @@ hipError_t launch_linear_few(const LinArgs& a, const LinPlan& p, int dtype, int 
 hipError_t launch_linear_tile(const LinArgs& a, const LinPlan& p, int dtype, int held, hipStream_t s);
 
 // ------------------------------------------------- products grouped by expert
-constexpr int kMaxGroups = 768;  // their first tiles and rows stand in LDS
+constexpr int kMaxGroups = 1024;  // their first tiles and rows stand in LDS
 
 struct GroupArgs {
     const void* x;
