@@ -345,6 +345,17 @@ hipError_t launch_few_t(const LinArgs& a, const LinPlan& p, hipStream_t s)
             return hipGetLastError();
         }
     }
+    if constexpr (X == kXI8) {
+        if (p.rb == 2 && p.nt < 4) {
+            if (a.tokens <= 8)
+                launch_few_k<T, X, 8, 2, 1, 8, 3>(a, s);
+            else if (p.nt == 1)
+                launch_few_k<T, X, 8, 2, 1, 16, 3>(a, s);
+            else
+                launch_few_k<T, X, 4, 2, 2, 32, 4>(a, s);
+            return hipGetLastError();
+        }
+    }
     if (a.tokens <= 8)
         launch_few_k<T, X, 8, 1, 1, 8, 4>(a, s);
     else if (p.nt == 1)

@@ -303,9 +303,19 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     // 17.0 (18.6); 256 tokens, 4096 to 1024, rank 32 23.4 (27.8), rank 64 30.7 (29.5);
     // 200 tokens, 8192 to 1024, rank 64 39 (47); 1024 tokens, 1024 to 256, rank 16 16.6
     // (13.6).
+    // 8-bit integers, whose rows are half as long, without adapters: 256 tokens, 2048
+    // to 1024 7.9 us (9.9 by tiles), 4096 to 1024 9.9 (16.6), 1024 to 512 6.0 (6.1).
+    const bool i8 = d.x_dtype == CVX_DT_I8;
     p.few = d.tokens <= 64 ||
-            (d.x_dtype == d.dtype && d.c_in >= 64 * (d.rank > 32 ? d.rank : 32) &&
+            ((d.x_dtype == d.dtype || i8) &&
+             (d.c_in >= 64 * (d.rank > 32 ? d.rank : 32) || (i8 && d.rank == 0)) &&
              (long)((d.c_out + 15) / 16) * ((d.tokens + 63) / 64) <= 256);
+    // Tiles drop nothing of 8-bit integers and take what would be more than a workgroup
+    // a compute unit here, but for few tokens of long rows.  4096 -> 10240 channels: 16
+    // tokens 14.5 us (15.2 by tiles), 32 18.0 (16.1), 64 24.7 (17.4); 4096 -> 14336: one
+    // token 14.2 (15.7), 16 16.5 (16.2), 64 25.4 (18.7); 2048 -> 16384: one 10.3 (9.7), 64
+    // 20.1 (11.1).  4096 -> 8192: 32 tokens 10.3 (15.5), 64 13.9 (16.8).
+    if (i8 && d.tokens <= 64) p.few = d.c_out <= 32 * 256 || (d.tokens <= 16 && d.c_in > 2048);
     // The adapter's A is read by every workgroup: 4096 channels to 4096 9.2 us (12.2 with
     // a launch of its own), to 8192 16.4 (18.4), to 12288 27.1 (27.3), to 14336 35.7
     // (33.7); 1024 to 16384 17.6 (20.7).
@@ -315,7 +325,9 @@ LinPlan linear_plan(const cvx_linear_desc& d)
     // 32 channels a workgroup where 16 would be more than a workgroup a compute unit:
     // 64 tokens, 4096 channels to 4096 12.6 us (15.5 with 32), to 5120 21.6 (15.9), to
     // 8192 22.2 (17.3).
-    p.rb = p.nt == 4 && d.c_out > 16 * 256 ? 2 : 1;
+    // Rows of 8-bit integers are half as long, so fewer tokens take 32 too: 4096 -> 8192
+    // channels 9.5 us (8.3) for 8 tokens, 10.4 (9.2) for 16, 12.3 (10.3) for 32.
+    p.rb = (p.nt == 4 || i8) && d.c_out > 16 * 256 ? 2 : 1;
     // The tile that ends first by what a stage (128 bytes of every row) and the rest
     // of a tile measured, in 10 ns, with the tiles one a compute unit.  4096 -> 4096
     // channels, bf16: 512 tokens 22 us as 128x64 (256 tiles; 31 as 128x128), 1024
@@ -375,7 +387,7 @@ void linear_describe(const cvx_linear_desc& d, const LinPlan& p, char* buf, int 
     if (p.few)
         snprintf(buf, len, "linear few %dx%d%s kernel=cvx::k_linear_few<%s, %d, %s, %d, %d, %d, %d, %d>", 16 * p.rb,
                  16 * p.nt, lora, t, held, p.one ? "true" : "false", p.nt == 1 ? 8 : 4, p.rb, p.nt,
-                 d.tokens <= 8 ? 8 : 16 * p.nt, p.nt == 4 || p.one ? 3 : 4);
+                 d.tokens <= 8 ? 8 : 16 * p.nt, p.nt == 4 || p.one || (p.rb == 2 && p.nt == 1) ? 3 : 4);
     else
         snprintf(buf, len, "linear tile %dx%d%s kernel=cvx::k_linear_tile<%s, %d, %s, 2, %d, %d, %d, %d>", 64 * p.mb, 64 * p.nb,
                  lora, t, held, d.rank ? "true" : "false", p.mb == 4 ? 4 : 2, p.mb, p.mb == 4 ? 2 : p.nb,

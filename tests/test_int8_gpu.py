@@ -218,7 +218,24 @@ def test_projection_with_adapters(t, ci, co, rank, n, kw):
     check(Case(t * 17 + rank, t, ci, co, rank=rank, n=n, **kw))
 
 
-@pytest.mark.parametrize("t,co,bn", [(2000, 8192, 256), (1500, 2560, 128), (300, 516, 64)])
+@pytest.mark.parametrize("t", [1, 8, 9, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("ci,co", [(2064, 4100), (1040, 8192), (528, 8196), (2064, 8200)])
+def test_few_tokens_of_wide_layers(t, ci, co):
+    # where the rules of few tokens change
+    check(Case(t + co, t, ci, co, res=2 if t % 2 else 0))
+    check(Case(t + co, t, ci, co, F16, rank=16, n=4, act=SILU))
+
+
+@pytest.mark.parametrize("t,ci,co,few", [(65, 256, 2048, True), (128, 272, 2048, True), (129, 272, 2052, False),
+                                         (1000, 64, 256, True), (1025, 64, 256, False), (256, 2064, 1024, True)])
+def test_many_tokens_of_narrow_layers(t, ci, co, few):
+    c = Case(t + co, t, ci, co, res=1, pads=(16, 4, 8))
+    assert (cvx.cvx_linear_plan(c.desc()).split()[1] == "few") == few
+    check(c)
+    check(Case(t + co, t, ci, co, F16, rank=8, n=4, act=RELU))
+
+
+@pytest.mark.parametrize("t,co,bn", [(2000, 8192, 256), (1500, 2560, 128), (300, 1028, 64)])
 def test_every_tile(t, co, bn):
     ci = 1040
     for kw in (dict(), dict(rank=16, n=3, dt=F16)):
