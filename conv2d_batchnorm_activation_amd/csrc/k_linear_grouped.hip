@@ -82,10 +82,10 @@ __device__ __forceinline__ void fetch64(rsrc_t r, unsigned off, void* to)
 }
 
 // WM x WN waves, each MB x NB blocks of 32 x 32; D stage buffers.
-template <typename T, int X, int WM, int WN, int MB, int NB, int D>
-__global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_grouped(GroupArgs a)
+template <typename T, int X, int WM, int WN, int MB, int NB, int D, int RB>
+__global__ void __launch_bounds__(64 * WM * WN, WM * WN == 8 || RB == 64 ? 2 : 1) k_linear_grouped(GroupArgs a)
 {
-    typedef Tile<T, X, WM, WN, MB, NB, D> tile;
+    typedef Tile<T, X, WM, WN, MB, NB, D, RB> tile;
     typedef typename tile::v4 v4;
     constexpr bool Q = X != kX16;  // 8-bit operands, tokens' scales
     constexpr unsigned XB = tile::XB;
@@ -271,11 +271,13 @@ hipError_t launch_grouped_t(GroupArgs a, const GroupPlan& p, hipStream_t s)
     a.tiles_m = (a.cout + 64 * p.mb - 1) / (64 * p.mb);
     const dim3 grid((unsigned)p.grid);
     if (p.mb == 4)
-        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 4, 4, 2, 2>), grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 4, 4, 2, 2, 128>), grid, dim3(512), 0, s, a);
     else if (p.nb == 2)
-        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 2, 4>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 2, 4, 128>), grid, dim3(256), 0, s, a);
+    else if (p.rb == 128)
+        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 1, 4, 128>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 1, 4>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 1, 4, 64>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -290,23 +292,33 @@ hipError_t launch_linear_grouped(const GroupArgs& a, const GroupPlan& p, int dty
 GroupPlan grouped_plan(const cvx_grouped_desc& d)
 {
     GroupPlan p;
+    // The tile that ends first by what a stage (128 bytes of every row) and the rest of a
+    // tile measured, in 10 ns, with the tiles one a compute unit (the last kind two, of
+    // half stages: one's end beside the other's products).  How the rows are spread is not
+    // known here: a group is taken to have a tile at least and to leave half a one empty.
+    // 351 cases, us as 256x256, 128x128, 128x64 and the last kind: 64 groups, 2048 ->
+    // 2816 bf16, 8 rows each 175, 151, 144, 145; 64 184, 163, 170, 191; 128 203, 209, 234,
+    // 252; 512 421, 533, 671, 773.  128 groups of e4m3, 512 -> 768, 8 rows each 25, 21, 19,
+    // 14.  Five of integers, 1008 -> 1284, 128 rows each 20, 10, 8.7, 9.4.  Over all, the kind
+    // taken needs 1.3% more time than the best, 54% at most (one group of 512 rows).
     const struct {
-        int mb, nb, stage, rest;
-    } tiles[] = {{4, 4, 150, 1000}, {2, 2, 45, 500}, {2, 1, 28, 400}};
+        int mb, nb, rb, at_once, stage, rest;
+    } tiles[] = {{4, 4, 128, 256, 130, 900}, {2, 2, 128, 256, 45, 400}, {2, 1, 128, 256, 36, 500}, {2, 1, 64, 512, 80, 100}};
     const long stages = ((long)d.c_in * (d.x_dtype == d.dtype ? 2 : 1) + 127) / 128;
     const long some = d.rows < d.n_groups ? d.rows : d.n_groups;  // groups that may have rows
     long best = -1;
     for (const auto& t : tiles) {
         const long m = (d.c_out + 64 * t.mb - 1) / (64 * t.mb);
-        const long n = m * ((d.rows + 64 * t.nb - 1) / (64 * t.nb) + some / 2);
-        const long time = (n + 255) / 256 * (stages * t.stage + t.rest);
+        const long tall = (d.rows + 64 * t.nb - 1) / (64 * t.nb) + some / 2, n = m * (tall < some ? some : tall);
+        const long time = (n + t.at_once - 1) / t.at_once * (stages * t.stage + t.rest);
         if (best >= 0 && time >= best) continue;
         best = time;
         p.mb = t.mb;
         p.nb = t.nb;
-        // a workgroup a compute unit, as many as there may be tiles
+        p.rb = t.rb;
+        // as many workgroups as run at once, or as there may be tiles
         const long most = m * (d.rows / (64 * t.nb) + some);
-        p.grid = (int)(most < 256 ? (most + 7) / 8 * 8 : 256);
+        p.grid = (int)(most < t.at_once ? (most + 7) / 8 * 8 : t.at_once);
     }
     return p;
 }
@@ -314,9 +326,9 @@ GroupPlan grouped_plan(const cvx_grouped_desc& d)
 void grouped_describe(const cvx_grouped_desc& d, const GroupPlan& p, char* buf, int len)
 {
     const char* t = d.dtype == CVX_DT_F16 ? "_Float16" : "__bf16";
-    snprintf(buf, len, "grouped tile %dx%d workgroups=%d kernel=cvx::k_linear_grouped<%s, %d, 2, %d, %d, %d, %d>", 64 * p.mb,
-             64 * p.nb, p.grid, t, held_of(d.dtype, d.x_dtype), p.mb == 4 ? 4 : 2, p.mb, p.mb == 4 ? 2 : p.nb,
-             p.mb == 4 ? 2 : 4);
+    snprintf(buf, len, "grouped tile %dx%d workgroups=%d kernel=cvx::k_linear_grouped<%s, %d, 2, %d, %d, %d, %d, %d>",
+             64 * p.mb, 64 * p.nb, p.grid, t, held_of(d.dtype, d.x_dtype), p.mb == 4 ? 4 : 2, p.mb,
+             p.mb == 4 ? 2 : p.nb, p.mb == 4 ? 2 : 4, p.rb);
 }
 
 }  // namespace cvx

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
     __shared__ float sx_lds[Q ? BN : 1];
     __shared__ int id_lds[LORA ? BN : 1];
+    static_assert(tile::W * 4096 <= SB, "a stage buffer is used again after the products");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;

@@ -31,19 +31,20 @@ struct TileRows {
 };
 
 // T: 16-bit type; X: what the operands are held in (kX16: T).  WM x WN waves, each
-// MB x NB blocks of 32 x 32; D stage buffers.
-template <typename T, int X, int WM, int WN, int MB, int NB, int D>
+// MB x NB blocks of 32 x 32; D stage buffers; a stage is RB bytes of every row.
+template <typename T, int X, int WM, int WN, int MB, int NB, int D, int RB = 128>
 struct Tile {
     static constexpr bool X8 = X == kXE4m3;
     static constexpr bool I8 = X == kXI8;
     static constexpr unsigned XB = X == kX16 ? 2 : 1;  // bytes of an operand's value
     static constexpr int W = WM * WN, NT = 64 * W;
     static constexpr int BM = 32 * WM * MB, BN = 32 * WN * NB;
-    static constexpr int FM = BM / (8 * W), FN = BN / (8 * W);  // fetches of eight rows a wave, per stage and operand
-    static constexpr int STEPS = X8 ? 2 : 4;
-    static constexpr int SB = (BM + BN) * 128;  // bytes of a stage
+    static constexpr int RF = 1024 / RB;                          // rows of a fetch
+    static constexpr int FM = BM / (RF * W), FN = BN / (RF * W);  // fetches a wave, per stage and operand
+    static constexpr int STEPS = RB / (X8 ? 64 : 32);
+    static constexpr int SB = (BM + BN) * RB;  // bytes of a stage
     static_assert(D == 2 || D == 4, "stage buffers");
-    static_assert(W * 4096 <= SB && MB % 2 == 0, "LDS is used again after the main loop");
+    static_assert(MB % 2 == 0, "values are stored 64 channels at a time");
     static_assert(W % 2 == 0, "a wave's fetches begin at rows 8 * wave + 16 * i");
     static_assert(FM <= 8 && FN <= 8, "fetches a wave");
     typedef typename V16<T>::v4 v4;
@@ -52,22 +53,27 @@ struct Tile {
     typedef typename std::conditional<I8, i32x16, f32x16>::type sum_t;
 
     // The 16-byte piece this lane fetches of its row of a fetch: the pieces of row r lie
-    // permuted, piece p at p ^ (r/2 % 8); the sixteen lanes of an operand read that go
-    // together (0-3, 12-15, 20-27 of 32, or the others) then fall in all of the banks.
+    // permuted, piece p at p ^ (r/2 % 8), of 64-byte rows at p ^ (r/4 % 4); the sixteen lanes
+    // of an operand read that go together (0-3, 12-15, 20-27 of 32, or the others) then
+    // fall in all of the banks.
     static __device__ __forceinline__ unsigned piece(int wave, int lane)
     {
+        if (RB == 64) return (unsigned)((lane & 3) ^ (lane >> 4)) * 16;
         return (unsigned)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4))) * 16;
     }
     // The row of the tile that this lane's part of fetch i is of.
-    static __device__ __forceinline__ int fetch_row(int wave, int lane, int i) { return 8 * (wave + W * i) + (lane >> 3); }
+    static __device__ __forceinline__ int fetch_row(int wave, int lane, int i)
+    {
+        return RF * (wave + W * i) + lane / (RB / 16);
+    }
 
     // The fetches of stage `st` of a tile into a stage buffer.
     static __device__ __forceinline__ void issue(const TileRows& o, unsigned cb, int st, unsigned char* buf, int wave,
                                                  int lane)
     {
         const unsigned pc = piece(wave, lane);
-        const unsigned kb = (unsigned)st * 128 < cb ? (unsigned)st * 128 : 0u;  // past the end: nothing is live
-        const unsigned dead = (unsigned)st * 128 + pc < cb ? 0u : kOOB;
+        const unsigned kb = (unsigned)st * RB < cb ? (unsigned)st * RB : 0u;  // past the end: nothing is live
+        const unsigned dead = (unsigned)st * RB + pc < cb ? 0u : kOOB;
         const char *wk = o.w + kb, *xk = o.x + kb;
         const unsigned wleft = o.wend - kb, xleft = o.xend - kb;
 #pragma unroll
@@ -77,7 +83,7 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(xk, xleft),
-                                                     (lds_void*)(buf + BM * 128 + 1024 * (wave + W * i)), 16,
+                                                     (lds_void*)(buf + BM * RB + 1024 * (wave + W * i)), 16,
                                                      o.xo[i] | dead, 0, 0, 0);
     }
     // The first D stages.
@@ -103,14 +109,15 @@ struct Tile {
     {
         const int wm = wave % WM, wn = wave / WM;
         const int hi = lane >> 5, l32 = lane & 31;
-        const int nst = (int)((cb + 127) / 128);
+        const int nst = (int)((cb + RB - 1) / RB);
         auto issue = [&](int st, unsigned char* buf) { Tile::issue(o, cb, st, buf, wave, lane); };
-        unsigned slot[4];
+        unsigned slot[RB / 32];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) slot[s] = (unsigned)(l32 * 128 + (((2 * s + hi) ^ ((l32 >> 1) & 7)) * 16));
+        for (int s = 0; s < RB / 32; ++s)
+            slot[s] = (unsigned)(l32 * RB + (((2 * s + hi) ^ (RB == 64 ? (l32 >> 2) & 3 : (l32 >> 1) & 7)) * 16));
         auto read = [&](const unsigned char* buf, int st, op_t(&A)[MB], op_t(&B)[NL]) {
-            const unsigned char* pa = buf + wm * MB * 4096;
-            const unsigned char* pb = buf + BM * 128 + wn * NL * 4096;
+            const unsigned char* pa = buf + wm * MB * 32 * RB;
+            const unsigned char* pb = buf + BM * RB + wn * NL * 32 * RB;
             auto one = [&](const unsigned char* p) {
                 if constexpr (X8) {
                     const u32x4 x = *reinterpret_cast<const u32x4*>(p + slot[2 * st]);
@@ -127,9 +134,9 @@ struct Tile {
                 }
             };
 #pragma unroll
-            for (int n = 0; n < NL; ++n) B[n] = one(pb + 4096 * n);
+            for (int n = 0; n < NL; ++n) B[n] = one(pb + 32 * RB * n);
 #pragma unroll
-            for (int m = 0; m < MB; ++m) A[m] = one(pa + 4096 * m);
+            for (int m = 0; m < MB; ++m) A[m] = one(pa + 32 * RB * m);
         };
 
 #pragma unroll
@@ -184,43 +191,54 @@ struct Tile {
             }
         };
         typedef std::integral_constant<int, FM + FN> fetch;
-        if constexpr (D == 2) {
+        if constexpr (W == 8) {
             // A step's operands are read under the step before.  Both loops take D stages;
             // those past the last are zeros, and so are the fetches past it.
             typedef std::integral_constant<int, 0> no_fetch;
             op_t A0[MB], B0[NL], A1[MB], B1[NL];
-            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
+            // A, B hold the first step's operands; where STEPS is odd, those of the next stage's
+            // first step are in An, Bn after it
+            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[MB], op_t(&B)[NL], op_t(&An)[MB],
+                             op_t(&Bn)[NL]) {
 #pragma unroll
                 for (int s = 0; s + 1 < STEPS; ++s) {
                     if (s & 1) {
-                        read(cur, s + 1, A0, B0);
-                        mul(A1, B1);
+                        read(cur, s + 1, A, B);
+                        mul(An, Bn);
                     } else {
-                        read(cur, s + 1, A1, B1);
-                        mul(A0, B0);
+                        read(cur, s + 1, An, Bn);
+                        mul(A, B);
                     }
                     mix(no_fetch());
                 }
-                wait_arrived<0>();  // the next stage has arrived, this wave has read the current one
+                wait_arrived<(D - 2) * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
                 stage_barrier();
-                issue(st + 2, cur);
-                read(nxt, 0, A0, B0);
-                mul(A1, B1);
+                issue(st + D, cur);
+                if constexpr (STEPS & 1) {
+                    read(nxt, 0, An, Bn);
+                    mul(A, B);
+                } else {
+                    read(nxt, 0, A, B);
+                    mul(An, Bn);
+                }
                 mix(fetch());
             };
-            if constexpr (BEGUN) {
-                wait_arrived<FM + FN>();
-                stage_barrier();
-            } else {
-                issue(0, buf0);
-                wait_arrived<0>();
-                stage_barrier();
-                issue(1, buf1);
-            }
+            if constexpr (!BEGUN) begin(o, cb, wave, lane, buf0, buf1, buf2, buf3);
+            wait_arrived<(D - 1) * (FM + FN)>();
+            stage_barrier();
             read(buf0, 0, A0, B0);
-            for (int st = 0; st < nst; st += 2) {
-                stage(st, buf0, buf1);
-                stage(st + 1, buf1, buf0);
+            constexpr bool ODD = STEPS & 1;
+            op_t(&A2)[MB] = ODD ? A1 : A0, (&A3)[MB] = ODD ? A0 : A1;
+            op_t(&B2)[NL] = ODD ? B1 : B0, (&B3)[NL] = ODD ? B0 : B1;
+            for (int st = 0; st < nst; st += D) {
+                stage(st, buf0, buf1, A0, B0, A1, B1);
+                if constexpr (D == 2) {
+                    stage(st + 1, buf1, buf0, A2, B2, A3, B3);
+                } else {
+                    stage(st + 1, buf1, buf2, A2, B2, A3, B3);
+                    stage(st + 2, buf2, buf3, A0, B0, A1, B1);
+                    stage(st + 3, buf3, buf0, A2, B2, A3, B3);
+                }
             }
         } else {
             // One wave a SIMD: a stage's operands are all read under the stage before, as

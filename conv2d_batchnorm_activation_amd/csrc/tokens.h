@@ -121,6 +121,7 @@ struct GroupArgs {
 
 struct GroupPlan {
     int mb, nb;            // tile: 64*mb channels x 64*nb rows
+    int rb;                // bytes of a row a stage
     int grid;              // workgroups, a multiple of eight
 };
 
