@@ -39,33 +39,6 @@ __device__ __forceinline__ float lane_move(float v)
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
-// 16x16 block, 64 bytes of k a row.  e4m3 values are widened to 16 bits, exactly:
-// the 8-bit matrix instructions drop what lies 2^-13 below the largest of eight
-// products, and here the stream of the weights leaves time for better.  Sums of 8-bit
-// integers are integers.
-template <typename T, int X, typename S>
-__device__ __forceinline__ S mma_piece(u32x4 w, u32x4 x, S c)
-{
-    if constexpr (X == kXE4m3) {
-        c = mma16<T>(widen8<T, X>(u32x2{w[0], w[1]}), widen8<T, X>(u32x2{x[0], x[1]}), c);
-        return mma16<T>(widen8<T, X>(u32x2{w[2], w[3]}), widen8<T, X>(u32x2{x[2], x[3]}), c);
-    } else if constexpr (X == kXI8) {
-        return mma16_i8(w, x, c);
-    } else {
-        return mma16<T>(w, x, c);
-    }
-}
-
-// Waits until at most N of this wave's vector-memory operations are under way;
-// no memory access moves across it.
-template <int N>
-__device__ __forceinline__ void wait_vm()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-// Waits until this wave's LDS reads have returned.
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
 // NT blocks of 16 tokens, of which XR rows (a multiple of eight) are loaded.  ONE:
 // a single token with an adapter of up to 16 ranks; the adapter's A goes along as
 // 16 more rows, in every workgroup, which for one token is less than a launch.

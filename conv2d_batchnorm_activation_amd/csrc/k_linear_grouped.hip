@@ -285,6 +285,7 @@ hipError_t launch_grouped_t(GroupArgs a, const GroupPlan& p, hipStream_t s)
 
 hipError_t launch_linear_grouped(const GroupArgs& a, const GroupPlan& p, int dtype, int held, hipStream_t s)
 {
+    if (p.few) return launch_grouped_few(a, p, dtype, held, s);
     return by_types(dtype, held,
                     [&](auto t, auto x) { return launch_grouped_t<typename decltype(t)::type, x.value>(a, p, s); });
 }
@@ -306,6 +307,18 @@ GroupPlan grouped_plan(const cvx_grouped_desc& d)
     } tiles[] = {{4, 4, 128, 256, 130, 900}, {2, 2, 128, 256, 45, 400}, {2, 1, 128, 256, 36, 500}, {2, 1, 64, 512, 80, 100}};
     const long stages = ((long)d.c_in * (d.x_dtype == d.dtype ? 2 : 1) + 127) / 128;
     const long some = d.rows < d.n_groups ? d.rows : d.n_groups;  // groups that may have rows
+    // At most a workgroup a compute unit of the kernel for few rows, or two of long rows:
+    // one row, 4096 -> 4096 channels bf16 9.3 us (17.9 by tiles), 8192 -> 1024 7.8 (28);
+    // eight rows in as many groups, 2048 -> 512 7.7 (11.8); two of 4096 -> 4096 15.3 (18.2);
+    // 16 of 1024 -> 512 11.0 (9.2), eight of 2048 -> 1408 14.8 (12.9).
+    const long blocks = (d.rows + 15 * some) / 16;  // of up to 16 rows, at most
+    const long few = (long)((d.c_out + 15) / 16) * blocks;
+    p.few = few <= 256 || (few <= 512 && stages >= 32);
+    if (p.few) {
+        p.mb = p.nb = p.rb = 0;
+        p.grid = (int)blocks;
+        return p;
+    }
     long best = -1;
     for (const auto& t : tiles) {
         const long m = (d.c_out + 64 * t.mb - 1) / (64 * t.mb);
@@ -317,7 +330,7 @@ GroupPlan grouped_plan(const cvx_grouped_desc& d)
         p.nb = t.nb;
         p.rb = t.rb;
         // as many workgroups as run at once, or as there may be tiles
-        const long most = m * (d.rows / (64 * t.nb) + some);
+        const long most = m * ((d.rows + (64 * t.nb - 1) * some) / (64 * t.nb));
         p.grid = (int)(most < t.at_once ? (most + 7) / 8 * 8 : t.at_once);
     }
     return p;
@@ -326,7 +339,11 @@ GroupPlan grouped_plan(const cvx_grouped_desc& d)
 void grouped_describe(const cvx_grouped_desc& d, const GroupPlan& p, char* buf, int len)
 {
     const char* t = d.dtype == CVX_DT_F16 ? "_Float16" : "__bf16";
-    snprintf(buf, len, "grouped tile %dx%d workgroups=%d kernel=cvx::k_linear_grouped<%s, %d, 2, %d, %d, %d, %d, %d>",
+    if (p.few)
+        snprintf(buf, len, "grouped few 16x16 workgroups=%d kernel=cvx::k_grouped_few<%s, %d, %d>",
+                 (d.c_out + 15) / 16 * p.grid, t, held_of(d.dtype, d.x_dtype), d.rows <= 8 ? 8 : 16);
+    else
+        snprintf(buf, len, "grouped tile %dx%d workgroups=%d kernel=cvx::k_linear_grouped<%s, %d, 2, %d, %d, %d, %d, %d>",
              64 * p.mb, 64 * p.nb, p.grid, t, held_of(d.dtype, d.x_dtype), p.mb == 4 ? 4 : 2, p.mb,
              p.mb == 4 ? 2 : p.nb, p.mb == 4 ? 2 : 4, p.rb);
 }

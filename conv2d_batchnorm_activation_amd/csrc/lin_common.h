@@ -96,6 +96,33 @@ __device__ __forceinline__ u32x4 widen8(u32x2 q)
     return __builtin_bit_cast(u32x4, o);
 }
 
+// 16x16 block, 64 bytes of k a row.  e4m3 values are widened to 16 bits, exactly:
+// the 8-bit matrix instructions drop what lies 2^-13 below the largest of eight
+// products, and here the stream of the weights leaves time for better.  Sums of 8-bit
+// integers are integers.
+template <typename T, int X, typename S>
+__device__ __forceinline__ S mma_piece(u32x4 w, u32x4 x, S c)
+{
+    if constexpr (X == kXE4m3) {
+        c = mma16<T>(widen8<T, X>(u32x2{w[0], w[1]}), widen8<T, X>(u32x2{x[0], x[1]}), c);
+        return mma16<T>(widen8<T, X>(u32x2{w[2], w[3]}), widen8<T, X>(u32x2{x[2], x[3]}), c);
+    } else if constexpr (X == kXI8) {
+        return mma16_i8(w, x, c);
+    } else {
+        return mma16<T>(w, x, c);
+    }
+}
+
+// Waits until at most N of this wave's vector-memory operations are under way;
+// no memory access moves across it.
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Waits until this wave's LDS reads have returned.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // f(type of the output, what x and w are held in), both as values that carry them.
 template <typename T>
 struct TypeOf {
@@ -113,6 +140,12 @@ hipError_t by_types(int dtype, int held, F f)
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes a lane into LDS, lane l's to to + 16*l, from byte `off` of the operand.
+__device__ __forceinline__ void fetch16(rsrc_t r, unsigned off, void* to)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, (int)off, 0, 0, 0);
+}
 
 // Waits until at most N of this wave's vector-memory operations (fetches into LDS
 // among them) are under way and what it read from LDS is here; no memory access

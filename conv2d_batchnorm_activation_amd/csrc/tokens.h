@@ -120,13 +120,15 @@ struct GroupArgs {
 };
 
 struct GroupPlan {
+    int few;               // 1: the kernel for few rows of few groups; 0: the tile kernel
     int mb, nb;            // tile: 64*mb channels x 64*nb rows
     int rb;                // bytes of a row a stage
-    int grid;              // workgroups, a multiple of eight
+    int grid;              // tile: workgroups, a multiple of eight; few: blocks of rows
 };
 
 GroupPlan grouped_plan(const cvx_grouped_desc& d);
 void grouped_describe(const cvx_grouped_desc& d, const GroupPlan& p, char* buf, int len);
+hipError_t launch_grouped_few(const GroupArgs& a, const GroupPlan& p, int dtype, int held, hipStream_t s);
 hipError_t launch_linear_grouped(const GroupArgs& a, const GroupPlan& p, int dtype, int held, hipStream_t s);
 
 }  // namespace cvx

@@ -160,6 +160,21 @@ def test_many_groups(n):
     check(Case(n, sizes, 64, 132, F16, I8, before=3, weight=True))
 
 
+@pytest.mark.parametrize("sizes,ci,co,kw", [
+    ([1], 4096, 4096, {}), ([0] * 63 + [1], 8192, 1024, dict(tokens=3)), ([0] * 64 + [2, 0, 1], 272, 64, dict(behind=5)),
+    ([1, 0, 0, 1] * 20, 144, 36, dict(tokens=9, bad=11, weight=True)), ([8], 2064, 20, dict(before=1, pads=(16, 4))),
+    ([16], 4112, 68, dict(act=SILU)), ([17, 0, 40, 3], 80, 132, dict(tokens=60, act=RELU, scale=False)),
+    ([0] * 200 + [5, 0, 33], 528, 80, dict(behind=2, bias=False, weight=True)), ([100], 64, 260, dict(pads=(32, 8)))])
+@pytest.mark.parametrize("dt,held", [(BF16, BF16), (F16, F16), (F16, E4M3), (BF16, I8)])
+def test_few_rows(sizes, ci, co, kw, dt, held):
+    kw = dict(kw)
+    if kw.get("bad") and not kw.get("tokens"):
+        del kw["bad"]
+    c = Case(sum(sizes) + ci, sizes, ci, co, dt, held, **kw)
+    assert cvx.cvx_linear_grouped_plan(c.desc()).split()[1] == "few"
+    check(c)
+
+
 def spread(seed, n, rows):
     """Sizes of n groups, uneven, `rows` in all."""
     g = torch.Generator().manual_seed(seed)
@@ -195,17 +210,21 @@ def offsets(c, values):
     [0, 10, 20, 30, 40], [5, 5, 5, 5, 5], [-9, 4, 90, 12, 13], [0, 30, 10, 20, 35], [2 ** 31 - 1] * 5, [-2 ** 31] * 5,
     [40, 0, 0, 0, 0], [0, -5, 7, -2 ** 31, 2 ** 31 - 1], [3, 39, 2, 41, 0]])
 @pytest.mark.parametrize("held", [BF16, I8])
-def test_ends_of_any_kind(values, held):
-    offsets(Case(5, [10] * 4, 80, 36, BF16, held), values)
+@pytest.mark.parametrize("co", [36, 1604])
+def test_ends_of_any_kind(values, held, co):
+    c = Case(5, [10] * 4, 80, co, BF16, held)
+    assert cvx.cvx_linear_grouped_plan(c.desc()).split()[1] == ("few" if co == 36 else "tile")
+    offsets(c, values)
 
 
-def test_nothing_to_do():
-    c = Case(6, [0] * 70, 64, 36, behind=9)
+@pytest.mark.parametrize("co", [36, 5000])
+def test_nothing_to_do(co):
+    c = Case(6, [0] * 70, 64, co, behind=9)
     got = c.run()
     assert not got.numel()
 
 
-@pytest.mark.parametrize("sizes", [[3, 2, 4], [100, 60, 130], [600, 300, 600]])
+@pytest.mark.parametrize("sizes", [[3, 2, 4], [20, 30, 40], [100, 60, 130], [600, 300, 600]])
 def test_infinities_and_nan_stay_with_their_group_and_row(sizes):
     nan, inf = float("nan"), float("inf")
     c = Case(8, sizes, 96, 516, act=RELU)
