@@ -101,6 +101,7 @@ class Case:
             live = (j >= 0) & (j < self.tokens)
             j = torch.where(live, j, 0)
             x, w = self.x[j].to(f) * live[:, None], self.w[d].to(f)
+            whole = x @ w.t()  # of integers: exact, also where it is zero
             if self.sx is not None:
                 x = x * self.sx[j].to(f)[:, None]
             if self.scale is not None:
@@ -111,7 +112,9 @@ class Case:
                 gx, gw = (m.abs().view(len(m), self.ci // 8, 8).amax(2) for m in (x, w))
                 err = err + 7 * 2.0 ** -13 * (gx @ gw.t())
             if self.held == I8:
-                mag = z.abs()
+                z = whole * self.sx[j].to(f)[:, None]
+                z = z * self.scale[d].to(f) if self.scale is not None else z
+                mag, err = z.abs(), U * z.abs()
             if self.bias is not None:
                 z, mag = z + self.bias[d].to(f), mag + self.bias[d].to(f).abs()
             z = z * torch.sigmoid(z) if self.act == SILU else torch.relu(z) if self.act == RELU else z
