@@ -356,7 +356,14 @@ LinPlan linear_plan(const cvx_linear_desc& d)
         // an adapter of its own), 1024 tokens 53 with 16 (50 with 64), 2048 98 with 16
         // (88 with 64), 4096 156 (137).  Up to 2047 tokens may be as many requests.
         // Slices of c_in until the first product's grid fills the device.
-        p.down_nb = d.tokens <= 64 ? 0 : d.tokens < 2048 ? 1 : 4;
+        // x in 8-bit integers, which a block of 16 waits longer for: one token too where all
+        // are few steps (of 1024 channels and 16 ranks), us with one and with 16, an adapter a
+        // token drawn and adapters in runs: 333 tokens, 1008 to 1284 channels, rank 8 14.1,
+        // 16.4 and 11.9, 11.9; 128, 4096 to 4096, rank 16 23.1, 31.4 and 20.8, 22.3; 1000,
+        // 1008 to 1284, rank 8 15.8, 17.5 and 13.6, 12.7; 128, 4096 to 4096, rank 64 42.4,
+        // 45.7 and 33.0, 27.5.
+        const long down_steps = (long)d.tokens * ((d.rank + 15) / 16) * ((d.c_in + kLoraChunk - 1) / kLoraChunk);
+        p.down_nb = d.tokens <= 64 || (i8 && down_steps <= 800) ? 0 : d.tokens < 2048 ? 1 : 4;
         p.down_rc = p.down_nb < 4 || d.rank <= 16 ? 1 : d.rank <= 32 ? 2 : 4;
         const int tok = p.down_nb ? 16 * p.down_nb : 1, step = p.down_nb == 4 ? kLoraMany : kLoraChunk;
         const long chunks = (d.c_in + step - 1) / step;

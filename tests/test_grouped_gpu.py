@@ -164,7 +164,7 @@ def test_many_groups(n):
 
 
 @pytest.mark.parametrize("sizes,ci,co,kw", [
-    ([1], 4096, 4096, {}), ([0] * 63 + [1], 8192, 1024, dict(tokens=3)), ([0] * 64 + [2, 0, 1], 272, 64, dict(behind=5)),
+    ([1], 4096, 4096, {}), ([0] * 9 + [1], 8192, 1024, dict(tokens=3)), ([0] * 64 + [2, 0, 1], 272, 64, dict(behind=5)),
     ([1, 0, 0, 1] * 20, 144, 36, dict(tokens=9, bad=11, weight=True)), ([8], 2064, 20, dict(before=1, pads=(16, 4))),
     ([16], 4112, 68, dict(act=SILU)), ([17, 0, 40, 3], 80, 132, dict(tokens=60, act=RELU, scale=False)),
     ([0] * 200 + [5, 0, 33], 528, 80, dict(behind=2, bias=False, weight=True)), ([100], 64, 260, dict(pads=(32, 8)))])
