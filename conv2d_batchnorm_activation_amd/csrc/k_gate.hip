@@ -46,32 +46,30 @@ __device__ __forceinline__ double exp64(double x)
     return __builtin_amdgcn_ldexp(p, (int)n);
 }
 
-template <int ACT>
-__device__ __forceinline__ double act64(double g)
+// The activations: SiLU, or ReLU (a NaN stays one) or none by `relu`.
+template <bool SILU>
+__device__ __forceinline__ double act64(double g, bool relu)
 {
-    if constexpr (ACT == CVX_ACT_RELU) return g < 0.0 ? 0.0 : g;  // a NaN stays one
-    if constexpr (ACT == CVX_ACT_SILU) {
+    if constexpr (SILU) {
         const double d = 1.0 + exp64(-g);
         double q = __builtin_amdgcn_rcp(d);  // good to 2^-26 or so: two steps double that twice
         q = fma(fma(-d, q, 1.0), q, q);
         q = fma(fma(-d, q, 1.0), q, q);
         return g * (d < 1.0e300 ? q : 0.0);  // (the steps make a NaN of an infinity)
     }
-    return g;
+    return relu && g < 0.0 ? 0.0 : g;
 }
 
 // In fp32.  FAST: by the hardware's exponential and reciprocal.  Of the exponential's
 // argument, -g*log2(e), the rounding leaves up to |g|*2^-24 of the result, so that it is
 // good to 2^-20 or so of the value where g is at least kDeep.
 constexpr float kDeep = -16.0f;
-template <int ACT, bool FAST>
-__device__ __forceinline__ float act32(float g)
+template <bool SILU, bool FAST>
+__device__ __forceinline__ float act32(float g, bool relu)
 {
-    if constexpr (ACT == CVX_ACT_RELU) return g < 0.0f ? 0.0f : g;
-    if constexpr (ACT == CVX_ACT_SILU && FAST)
-        return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.442695041f));
-    if constexpr (ACT == CVX_ACT_SILU) return g / (1.0f + expf(-g));
-    return g;
+    if constexpr (SILU && FAST) return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.442695041f));
+    if constexpr (SILU) return g / (1.0f + expf(-g));
+    return relu && g < 0.0f ? 0.0f : g;
 }
 
 // VEC values of an operand from channel i0, zero past c.
@@ -118,19 +116,20 @@ __device__ __forceinline__ bool codes32(const float (&u)[VEC], float most, float
 }
 
 // 8-bit output: TPR threads a row.
-template <typename T, int TPR, int NV, int ACT, bool UP, int OUT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 1) k_gate(GateArgs a)
+template <typename T, int TPR, int NV, bool SILU, bool UP, int OUT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 4) k_gate(GateArgs a)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
     constexpr int HOLD = NV > 0 ? NV : 1;
     typedef typename Vec<T, VEC>::type V;
     const int lane = threadIdx.x % TPR;
     const long row = TPR < 256 ? (long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR : (long)blockIdx.x;
-    if (row >= a.rows) return;  // whole waves: a row has at least one
+    if (row >= a.rows) return;  // all threads of a row
     const T* g = static_cast<const T*>(a.gate) + row * a.gs;
     const T* p = UP ? static_cast<const T*>(a.up) + row * a.us : nullptr;
     unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.ys;
     const int c = a.c, nvec = (c + VEC - 1) / VEC;
+    const bool relu = a.act == CVX_ACT_RELU;
 
     V gv[HOLD], uv[UP ? HOLD : 1];
     auto load = [&](int v, int j) {
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 1) k_gate
         if constexpr (UP) uv[UP ? j : 0] = load_vec<T, VEC>(p, v * VEC, c);
     };
     auto exact = [&](int j, int e) {
-        const double x = act64<ACT>((double)(float)gv[j][e]);
+        const double x = act64<SILU>((double)(float)gv[j][e], relu);
         return UP ? x * (double)(float)uv[UP ? j : 0][e] : x;
     };
     // calls f(vector's index, its slot) for every vector of this thread, loaded before
@@ -161,13 +160,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 1) k_gate
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const float gf = (float)gv[j][e];
-            u[j][e] = act32<ACT, true>(gf);
+            u[j][e] = act32<SILU, true>(gf, relu);
             if constexpr (UP) u[j][e] *= (float)uv[UP ? j : 0][e];
             low = fminf(low, gf);
             m = fmaxf(m, fabsf(u[j][e]));
             if (e % 2) odd = fmaf(u[j][e], u[j][e - 1], odd);  // a NaN or an infinity from either on
         }
-        const bool told = fabsf(odd) < __builtin_inff() && (ACT != CVX_ACT_SILU || low >= kDeep);
+        const bool told = fabsf(odd) < __builtin_inff() && (!SILU || low >= kDeep);
         most[j] = told ? m : __builtin_inff();
     };
     float top = 0.0f;
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 1) k_gate
         near(j);
         top = fmaxf(top, most[j] < __builtin_inff() ? most[j] : 0.0f);
     });
-    top = row_max<TPR>(top);
+    top = row_top<TPR, 0>(top);
 
     // t, in 64 bits: the largest of the vectors that may hold it, those that fp32 does
     // not tell among them
@@ -185,20 +184,21 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 1) k_gate
     double t = 0.0, bad = 0.0;
     each([&](int, int j) {
         if constexpr (NV == 0) near(j);
-        if (!wide && most[j] < least) return;
+        const bool all = wide || most[j] == __builtin_inff();
+        if (!all && most[j] < least) return;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const double x = exact(j, e);
-            t = fmax(t, fabs(x));
-            bad = fma(x, 0.0, bad);
-        }
+        for (int e = 0; e < VEC; ++e)
+            if (all || fabsf(u[j][e]) >= least) {
+                const double x = exact(j, e);
+                t = fmax(t, fabs(x));
+                bad = fma(x, 0.0, bad);
+            }
     });
     if (bad != 0.0) t = __builtin_inf();
-    double none = 0.0;
-    row_reduce<TPR, true>(none, t);
+    t = row_top<TPR, 1>(t);
     const bool lost = t > 1.7e308;
     const double f = t > 0.0 && !lost ? kTop<OUT> * (1.0 / t) : 0.0;
-    if (lane == 0) a.y_scale[row] = lost ? __builtin_nanf("") : (float)(t / kTop<OUT>);
+    if (lane == 0) a.y_scale[row] = lost ? __builtin_nanf("") : (float)(t * (1.0 / kTop<OUT>));
 
     // codes from fp32 where it tells them, else from 64 bits
     each([&](int v, int j) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 1) k_gate
 }
 
 // Output of the inputs' type: a thread a vector.
-template <typename T, int ACT, bool UP>
+template <typename T, bool SILU, bool UP>
 __global__ void __launch_bounds__(256) k_gate_wide(GateArgs a)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(256) k_gate_wide(GateArgs a)
     float g[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        g[e] = act32<ACT, false>((float)gv[e]);
+        g[e] = act32<SILU, false>((float)gv[e], a.act == CVX_ACT_RELU);
         if constexpr (UP) g[e] *= (float)uv[e];
     }
     T* y = static_cast<T*>(a.y) + row * a.ys;
@@ -249,22 +249,20 @@ __global__ void __launch_bounds__(256) k_gate_wide(GateArgs a)
     }
 }
 
-// f(the activation, whether there is an `up`), as values that carry them
+// f(whether the activation is SiLU, whether there is an `up`), as values that carry them
 template <typename F>
 void by_act(const GateArgs& a, F f)
 {
-    auto of = [&](auto act) {
+    auto of = [&](auto silu) {
         if (a.up)
-            f(act, std::true_type());
+            f(silu, std::true_type());
         else
-            f(act, std::false_type());
+            f(silu, std::false_type());
     };
     if (a.act == CVX_ACT_SILU)
-        of(std::integral_constant<int, CVX_ACT_SILU>());
-    else if (a.act == CVX_ACT_RELU)
-        of(std::integral_constant<int, CVX_ACT_RELU>());
+        of(std::true_type());
     else
-        of(std::integral_constant<int, CVX_ACT_NONE>());
+        of(std::false_type());
 }
 
 template <typename T, int TPR, int NV>
@@ -272,11 +270,11 @@ void launch_rows(const GateArgs& a, hipStream_t s)
 {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     const dim3 grid((unsigned)(((long)a.rows + RPB - 1) / RPB)), block(TPR < 256 ? 256 : TPR);
-    by_act(a, [&](auto act, auto up) {
+    by_act(a, [&](auto silu, auto up) {
         if (a.held == kXE4m3)
-            hipLaunchKernelGGL((k_gate<T, TPR, NV, act.value, up.value, kXE4m3>), grid, block, 0, s, a);
+            hipLaunchKernelGGL((k_gate<T, TPR, NV, silu.value, up.value, kXE4m3>), grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL((k_gate<T, TPR, NV, act.value, up.value, kXI8>), grid, block, 0, s, a);
+            hipLaunchKernelGGL((k_gate<T, TPR, NV, silu.value, up.value, kXI8>), grid, block, 0, s, a);
     });
 }
 
@@ -287,19 +285,29 @@ hipError_t launch_t(const GateArgs& a, hipStream_t s)
     const long nvec = ((long)a.c + VEC - 1) / VEC;
     if (a.held == kX16) {
         const dim3 grid((unsigned)((a.rows * nvec + 255) / 256));
-        by_act(a, [&](auto act, auto up) {
-            hipLaunchKernelGGL((k_gate_wide<T, act.value, up.value>), grid, dim3(256), 0, s, a);
+        by_act(a, [&](auto silu, auto up) {
+            hipLaunchKernelGGL((k_gate_wide<T, silu.value, up.value>), grid, dim3(256), 0, s, a);
         });
+    } else if (nvec <= 16) {
+        // Short rows are 16 threads' or a wave's, which needs no barrier: us as 256 threads'
+        // rows and as these, 32768 rows of 1408 bf16 channels 85 and 47, 65536 of 512 (a wave
+        // each) 66 and 37, 500000 of 64 447 and 84.  Long ones are held as long as there
+        // are registers: 4096 of 20480 146 read anew, 108 held.
+        launch_rows<T, 16, 1>(a, s);
     } else if (nvec <= 64) {
-        launch_rows<T, 64, 1>(a, s);
+        launch_rows<T, 16, 4>(a, s);
     } else if (nvec <= 256) {
-        launch_rows<T, 256, 1>(a, s);
+        launch_rows<T, 64, 4>(a, s);
     } else if (nvec <= 512) {
         launch_rows<T, 256, 2>(a, s);
     } else if (nvec <= 1024) {
         launch_rows<T, 1024, 1>(a, s);
     } else if (nvec <= 2048) {
         launch_rows<T, 1024, 2>(a, s);
+    } else if (nvec <= 4096) {
+        launch_rows<T, 1024, 4>(a, s);
+    } else if (VEC == 4 && nvec <= 6144) {
+        launch_rows<T, 1024, VEC == 4 ? 6 : 0>(a, s);
     } else {
         launch_rows<T, 1024, 0>(a, s);
     }

@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "tokens.h"
 
 namespace cvx {
@@ -106,25 +108,45 @@ __device__ __forceinline__ double wave_all(double v, OP op)
     return op(op(lane_value<0>(v), lane_value<16>(v)), op(lane_value<32>(v), lane_value<48>(v)));
 }
 
-// The largest of the row's TPR threads' values, none of them a NaN.
-template <int TPR>
-__device__ __forceinline__ float row_max(float v)
+// The largest of the values of a row's TPR threads (16, or whole waves), none of them a
+// NaN.  S: which of a kernel's exchanges by way of LDS this is.
+template <int TPR, int S, typename V>
+__device__ __forceinline__ V row_top(V v)
 {
-    auto bits = [](float f) { return __builtin_bit_cast(int, f); };
-    auto value = [](int i) { return __builtin_bit_cast(float, i); };
-    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0xb1, 0xf, 0xf, true)));
-    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0x4e, 0xf, 0xf, true)));
-    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0x141, 0xf, 0xf, true)));
-    v = fmaxf(v, value(__builtin_amdgcn_mov_dpp(bits(v), 0x140, 0xf, 0xf, true)));
-    auto lane = [&](int l) { return value(__builtin_amdgcn_readlane(bits(v), l)); };
-    v = fmaxf(fmaxf(lane(0), lane(16)), fmaxf(lane(32), lane(48)));
+    constexpr bool F = sizeof(V) == 4;
+    auto move = [](V x, auto ctrl) {
+        if constexpr (F)
+            return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
+        else
+            return lane_move<decltype(ctrl)::value>(x);
+    };
+    auto larger = [](V x, V y) {
+        if constexpr (F)
+            return fmaxf(x, y);
+        else
+            return fmax(x, y);
+    };
+    v = larger(v, move(v, std::integral_constant<int, 0xb1>()));
+    v = larger(v, move(v, std::integral_constant<int, 0x4e>()));
+    v = larger(v, move(v, std::integral_constant<int, 0x141>()));
+    v = larger(v, move(v, std::integral_constant<int, 0x140>()));
+    if constexpr (TPR > 16) {
+        auto of = [&](auto lane) {
+            if constexpr (F)
+                return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), decltype(lane)::value));
+            else
+                return lane_value<decltype(lane)::value>(v);
+        };
+        v = larger(larger(of(std::integral_constant<int, 0>()), of(std::integral_constant<int, 16>())),
+                   larger(of(std::integral_constant<int, 32>()), of(std::integral_constant<int, 48>())));
+    }
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
-        __shared__ float lv[W];
-        if ((threadIdx.x & 63) == 0) lv[threadIdx.x >> 6] = v;
+        __shared__ V tops[W];
+        if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = v;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < W; ++i) v = fmaxf(v, lv[i]);
+        for (int i = 0; i < W; ++i) v = larger(v, tops[i]);
     }
     return v;
 }

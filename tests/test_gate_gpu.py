@@ -89,7 +89,7 @@ def rows_of(seed, rows, c, dt, size=1.0):
 
 
 SIZES = [(1, 1), (1, 4096), (3, 7), (2, 64), (5, 513), (300, 1337), (33, 2048), (129, 4104), (7, 8200), (2, 14336), (3, 20481),
-         (2, 40000)]
+         (2, 40000), (37, 130), (1001, 300), (70, 512), (17, 128), (2, 33000)]
 
 
 @pytest.mark.parametrize("rows,c", SIZES)
