@@ -7,12 +7,13 @@
 // Bound by memory: every value is read once and written once.  With 8-bit output a
 // row's largest magnitude is one reduction between the TPR threads that hold it, as NV
 // 16-byte vectors an operand each; rows too long to be held (NV = 0) are read a second
-// time.  t and the codes are those of 64-bit values, so that a code is the nearest to
-// its value and integers do not depend on how an exponential was rounded.  Few values
-// need 64 bits for that: those that may be the largest, and those that fp32 leaves at a
-// border between two codes.  With 64 bits for all (some 35 instructions a value) 8192
-// rows of 14336 bf16 channels took 236 us; they take 112, 5.2 TB/s.  Output of the inputs' type is u in fp32,
-// and there is no row: a thread takes a vector.
+// time.  t and the codes are those of 64-bit values, by the formula's own steps: where
+// u/t is a ratio of small integers, u*(M*(1/t)) can be a border between two codes but
+// for the last bit of either, and then only the same roundings give the same code.  Few
+// values need 64 bits: those that may be the largest, and those that fp32 leaves at a
+// border.  With 64 bits for all (some 35 instructions a value) 8192 rows of 14336 bf16
+// channels took 236 us; they take 110, 5.3 TB/s.  Output of the inputs' type is u in
+// fp32, and there is no row: a thread takes a vector.
 #include <type_traits>
 
 #include "cvx_internal.h"
@@ -22,52 +23,27 @@ namespace cvx {
 
 namespace {
 
-// exp(x), x clamped to where the result is 0, finite or infinite: 2^n * e^r with
-// |r| <= ln(2)/2 and the series of e^r to r^12, which leaves 2e-16 of it.
-__device__ __forceinline__ double exp64(double x)
-{
-    x = fmin(fmax(x, -1100.0), 1100.0);
-    const double n = rint(x * 1.4426950408889634);
-    double r = fma(-n, 0x1.62e42fefa39efp-1, x);  // ln(2) to 53 bits, and what is left of it
-    r = fma(-n, 0x1.abc9e3b39803fp-56, r);
-    double p = 1.0 / 479001600.0;
-    p = fma(p, r, 1.0 / 39916800.0);
-    p = fma(p, r, 1.0 / 3628800.0);
-    p = fma(p, r, 1.0 / 362880.0);
-    p = fma(p, r, 1.0 / 40320.0);
-    p = fma(p, r, 1.0 / 5040.0);
-    p = fma(p, r, 1.0 / 720.0);
-    p = fma(p, r, 1.0 / 120.0);
-    p = fma(p, r, 1.0 / 24.0);
-    p = fma(p, r, 1.0 / 6.0);
-    p = fma(p, r, 0.5);
-    p = fma(p, r, 1.0);
-    p = fma(p, r, 1.0);
-    return __builtin_amdgcn_ldexp(p, (int)n);
-}
-
 // The activations: SiLU, or ReLU (a NaN stays one) or none by `relu`.
 template <bool SILU>
 __device__ __forceinline__ double act64(double g, bool relu)
 {
-    if constexpr (SILU) {
-        const double d = 1.0 + exp64(-g);
-        double q = __builtin_amdgcn_rcp(d);  // good to 2^-26 or so: two steps double that twice
-        q = fma(fma(-d, q, 1.0), q, q);
-        q = fma(fma(-d, q, 1.0), q, q);
-        return g * (d < 1.0e300 ? q : 0.0);  // (the steps make a NaN of an infinity)
-    }
+    if constexpr (SILU) return g / (1.0 + exp(-g));
     return relu && g < 0.0 ? 0.0 : g;
 }
 
-// In fp32.  FAST: by the hardware's exponential and reciprocal.  Of the exponential's
-// argument, -g*log2(e), the rounding leaves up to |g|*2^-24 of the result, so that it is
-// good to 2^-20 or so of the value where g is at least kDeep.
-constexpr float kDeep = -16.0f;
+// In fp32.  FAST: by the hardware's exponential and reciprocal (an ulp each), with what
+// rounding the exponential's argument, -g*log2(e), left as a factor: off by less than
+// 2*2^-23 + 4*2^-24 of the value where g is at least kDeep (below, 1/exp leaves fp32).
+constexpr float kDeep = -80.0f;
 template <bool SILU, bool FAST>
 __device__ __forceinline__ float act32(float g, bool relu)
 {
-    if constexpr (SILU && FAST) return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.442695041f));
+    if constexpr (SILU && FAST) {
+        const float x = g * -1.442695041f;
+        const float left = fmaf(g, -1.9259629911e-8f, fmaf(g, -1.442695041f, -x));
+        const float e = __builtin_amdgcn_exp2f(x);
+        return g * __builtin_amdgcn_rcpf(1.0f + fmaf(e, left * 0.6931471806f, e));
+    }
     if constexpr (SILU) return g / (1.0f + expf(-g));
     return relu && g < 0.0f ? 0.0f : g;
 }
@@ -84,9 +60,19 @@ __device__ __forceinline__ typename Vec<T, VEC>::type load_vec(const T* p, int i
     return v;
 }
 
-// The codes of VEC values u*f, from fp32; true if one of them may be another, u being
-// off by less than kOff of itself, none larger than `most`.
-constexpr float kOff = 0x1p-19f;
+// More than an fp32 u*f is off by, of itself: u 2*2^-23 + 5*2^-24 with its second factor,
+// f half an ulp, twice and a half of the sum.
+constexpr float kOff = 1.5f * 0x1p-20f;
+
+// How far u*f is off the integer next to it.
+__device__ __forceinline__ float off_ones(float u, float f, float& ones)
+{
+    ones = fmaf(u, f, 0x1.8p23f);  // a sum that leaves none below one
+    return fabsf(fmaf(u, f, 0x1.8p23f - ones));
+}
+
+// The codes of VEC values u*f, from fp32; true if one of them may be another, none
+// being larger than `most`.
 template <int OUT, int VEC>
 __device__ __forceinline__ bool codes32(const float (&u)[VEC], float most, float f, unsigned (&w)[VEC / 4])
 {
@@ -100,13 +86,13 @@ __device__ __forceinline__ bool codes32(const float (&u)[VEC], float most, float
         }
         return any;
     }
-    unsigned ones[VEC];  // a sum that leaves none below one
-    float off = 0.0f;    // the most that a value is off its integer
+    unsigned ones[VEC];
+    float off = 0.0f;  // the most that a value is off its integer
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-        const float s = fmaf(u[e], f, 0x1.8p23f);
+        float s;
+        off = fmaxf(off, off_ones(u[e], f, s));
         ones[e] = __builtin_bit_cast(unsigned, s);
-        off = fmaxf(off, fabsf(fmaf(u[e], f, 0x1.8p23f - s)));
     }
 #pragma unroll
     for (int q = 0; q < VEC; q += 4)
@@ -205,10 +191,17 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 4) k_gate
         unsigned w[VEC / 4];
         if constexpr (NV == 0) near(j);
         bool any = codes32<OUT, VEC>(u[j], most[j], (float)f, w);
-        if (any || wide || most[j] == __builtin_inff()) {
+        const bool all = wide || most[j] == __builtin_inff();
+        if (any || all) {
             unsigned x[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) x[e] = code_part<OUT>(exact(j, e) * f);
+            for (int e = 0; e < VEC; ++e) {
+                float s;
+                const float off = off_ones(u[j][e], (float)f, s);
+                x[e] = __builtin_bit_cast(unsigned, s);
+                if (OUT != kXI8 || all || off > 0.5f - (fabsf(u[j][e]) * (float)f + 1.0f) * kOff)
+                    x[e] = code_part<OUT>(exact(j, e) * f);
+            }
 #pragma unroll
             for (int q = 0; q < VEC / 4; ++q) w[q] = pack_codes<OUT>(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
         }

@@ -4,9 +4,12 @@ Tolerances.  16- and 32-bit output: the activation is good to 8 units of fp32 (a
 an addition, a quotient) where its exponent is small, and its exponential to |g|*2^-23 more of
 the value; the product is rounded once more, and the output once, eps/2 or half the smallest
 subnormal of its type.  Codes are the integers, or e4m3 values, nearest to u*(M*(1/t)), which both
-sides take in 64 bits: equal for the activations that are exact; where an exponential comes in,
-the two sides' u differ by some 2^-50 of it, and a code may differ where u*f lies that
-near to a border, which none of these seeds' values does.  y_scale is rounded once to fp32."""
+sides take in 64 bits: equal for the activations that are exact.  Where an exponential comes in,
+the two sides' u may differ by some 2^-50 of it, and a code where u*f lies that near to a
+border: where another value's gate is the same and its factor a simple multiple, so that u/t
+is a ratio of small integers.  The test of many values meets such pairs and takes its
+64-bit values on the GPU, where the exponential is the same; the small tests' seeds have none.
+y_scale is rounded once to fp32."""
 import pytest
 import torch
 
@@ -187,6 +190,37 @@ def test_borders(dt):
     for out in (I8, E4M3):
         check(g, p, dt, out, NONE)
         check(g, None, dt, out, RELU)
+
+
+@pytest.mark.parametrize("out", [I8, E4M3])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("spread", ["normal", "wide", "deep"])
+def test_many_values(dt, out, spread):
+    # hundreds of millions of values: the few whose codes fp32 does not tell are among them
+    r = torch.Generator(device=DEV).manual_seed(dt + out)
+    rows, c = 4096, 14336
+    for _ in range(3):
+        size = torch.exp(0.5 * torch.randn(c, generator=r, device=DEV))
+        g = torch.randn(rows, c, generator=r, device=DEV) * size
+        if spread != "normal":  # gates down to where the exponential ends, factors that make up for it
+            g = 90 * torch.rand(rows, c, generator=r, device=DEV) - 85
+        p = torch.randn(rows, c, generator=r, device=DEV)
+        if spread != "normal":
+            p = p * torch.exp(torch.relu(-g)) * (30 if spread == "wide" else 3)  # 30: some are infinite
+        g, p = g.to(DT[dt]), p.to(DT[dt])
+        y, q = torch.empty(rows, c, dtype=DT[out], device=DEV), torch.empty(rows, device=DEV)
+        say(f"gate of many values, dt={dt} out={out} {spread}")
+        cvx.cvx_gate(cvx.make_gate_desc(rows, c, dt, out), g, p, y, q)
+        for a in range(0, rows, 512):
+            u = value(g[a:a + 512], p[a:a + 512], SILU)
+            t = u.abs().amax(1)
+            told = torch.isfinite(t)  # a row with an infinity has a NaN scale
+            assert torch.equal(torch.isfinite(q[a:a + 512]), told) and (told.all() or spread == "wide")
+            u, t, got, scale = u[told], t[told], y[a:a + 512][told], q[a:a + 512][told].double()
+            v = u * (MOST[out] * (1.0 / t))[:, None]
+            want = torch.round(v) if out == I8 else nearest_e4m3(v)
+            assert torch.equal(got.double() if out == I8 else got.float().double(), want)
+            assert ((scale - t / MOST[out]).abs() <= 2 * U * t / MOST[out]).all()
 
 
 def test_far_rows_streams_and_graphs():
