@@ -44,7 +44,10 @@ __device__ __forceinline__ float act32(float g, bool relu)
         const float e = __builtin_amdgcn_exp2f(x);
         return g * __builtin_amdgcn_rcpf(1.0f + fmaf(e, left * 0.6931471806f, e));
     }
-    if constexpr (SILU) return g / (1.0f + expf(-g));
+    if constexpr (SILU) {  // by the exponential that does not overflow: the value down to where fp32 ends
+        const float e = expf(-fabsf(g));
+        return (g < 0.0f ? g * e : g) / (1.0f + e);
+    }
     return relu && g < 0.0f ? 0.0f : g;
 }
 
@@ -314,7 +317,7 @@ hipError_t launch_gate(const GateArgs& all, int dtype, hipStream_t s)
     // as many rows a launch as keep a grid below 2^32 threads
     const long es = dtype == CVX_DT_F32 ? 4 : 2, eo = all.held != kX16 ? 1 : es;
     const long nvec = (all.c + 16 / es - 1) / (16 / es);
-    const long most = all.held != kX16 ? 1l << 20 : nvec < (1l << 31) ? (1l << 31) / nvec : 1;
+    const long most = all.held != kX16 ? 1l << 20 : (1l << 31) / nvec;
     for (long r0 = 0; r0 < all.rows; r0 += most) {
         GateArgs a = all;
         a.rows = (int)(all.rows - r0 < most ? all.rows - r0 : most);

@@ -183,6 +183,31 @@ def test_rows_of_mixed_sizes(c, dt):
 
 
 @pytest.mark.parametrize("dt", [BF16, F32])
+def test_deep_gates(dt):
+    # down to where SiLU itself leaves fp32, with factors that bring it back: SiLU is off by a few
+    # roundings of its own or, below the normal numbers, by half the smallest of them and |g| times
+    # half of it in exp(g) (two halves, the library's exponential being within one), all times |p|
+    r = torch.Generator().manual_seed(dt)
+    g = -70 - 40 * torch.rand(40, 333, generator=r)
+    p = 1e30 * torch.randn(40, 333, generator=r)
+    g, p = g.to(DT[dt]), p.to(DT[dt])
+    got, _ = run(g, p, dt, dt, SILU)
+    u = value(g, p, SILU)
+    fi = torch.finfo(DT[dt])
+    part = (10 + 2 * g.double().abs()) * U * u.abs() + (0.5 + g.double().abs()) * 2.0 ** -149 * p.double().abs()
+    assert ((got - u).abs() <= part + (fi.eps / 2) * (u.abs() + part) + fi.smallest_normal * fi.eps).all()
+    assert ((u == 0) == (got == 0))[g > -85].all()
+
+
+def test_rows_of_more_than_one_launch():
+    r = torch.Generator().manual_seed(11)
+    rows = (1 << 20) + 77
+    g, p = (torch.randn(rows, 8, generator=r).to(torch.bfloat16) for _ in range(2))
+    for out in (I8, E4M3):
+        check(g, p, BF16, out, NONE, (0, 4, 3))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
 def test_borders(dt):
     # products of few values: many u*M/t lie at a border, or a rounding off it
     r = torch.Generator().manual_seed(4)
