@@ -18,7 +18,9 @@
 // Measured, the rate that of the weights: one token, 4096 -> 4096 channels bf16 7.5
 // us (4.5 TB/s), with an adapter of rank 16 8.7; 16 tokens of e4m3, 8192 -> 8192
 // 15.0 (4.5), with 16 adapters of rank 16 21.3; 48 tokens bf16, 4096 -> 8192 16.6
-// (4.0), with 32 adapters of rank 32 34.  A copy of such weights runs at 5.4 TB/s;
+// (4.0), with 32 adapters of rank 32 34.  8-bit integers, summed as such: one token, 4096
+// -> 4096 4.4 to 5.8 (6.5 with the call), 48 tokens, 4096 -> 8192 with a residual 13.5
+// (2.6 TB/s: half the bytes between the same start and end).  A copy of such weights runs at 5.4 TB/s;
 // what is missing is a workgroup's first fetch and its end, as each compute unit
 // has one or two workgroups in all.  With a residual or adapters what the end needs
 // is loaded ahead of the first products (below), and only the stages fetched before

@@ -26,7 +26,9 @@
 // one channel in 64 a hundred times larger (fp32 sums: 3e-8, 5e-8).  The output's
 // own rounding is 1.7e-3 in bf16 and 2.1e-4 in fp16, which becomes 2.2e-4 with such
 // channels.  Taken for the rate: the same product of values held in 16 bits, whose
-// sums are fp32, is 726 us.
+// sums are fp32, is 726 us.  8-bit integers take the 32x32x32 instruction, whose sums
+// are exact: 8192 x 4096 x 14336 388 to 430 us over runs (2240 to 2480 TOPS; the
+// library's product 501); 512 tokens, 4096 -> 4096 13.4.
 //
 // Adapters: once the sums stand in registers they get scale and bias, and the
 // second product of the adapters is accumulated onto them by the same matrix

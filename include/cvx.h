@@ -522,9 +522,10 @@ CVX_API cvx_status cvx_linear_grouped_plan(const cvx_grouped_desc *d, char *buf,
  * one below an end before it as the largest before it.  Rows before the first group or
  * behind the last are left as they are.  A row whose row_id is negative or not below
  * `tokens` is taken as zeros.  Sums are those of cvx_linear: exact for 8-bit integers,
- * else in fp32, of e4m3 operands as it says for more than 64 tokens.  y is rounded once.  A group's weights, infinities and NaN included, reach
- * its rows and no others, and so does a row of x; a NaN stays one through every
- * activation.  Results do not depend on timing.
+ * else in fp32, of e4m3 operands as it says for more than 64 tokens.  y is rounded once.
+ * A group's weights, infinities and NaN included, reach its rows and no others, and so
+ * does a row of x; a NaN stays one through every activation.  Results do not depend on
+ * timing.
  *   x         : device [tokens][c_in] of x_dtype, 16-byte aligned rows; with row_id, at
  *               most 2^31 bytes from first to last.
  *   x_scale   : device fp32 [tokens]; required iff x_dtype is an 8-bit type.
