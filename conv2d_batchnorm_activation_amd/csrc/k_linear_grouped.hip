@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN == 8 || RB == 64 ? 2 : 1
     constexpr unsigned XB = tile::XB;
     constexpr int W = tile::W, NT = tile::NT, BM = tile::BM, BN = tile::BN, SB = tile::SB;
     constexpr int TOK = 16;  // rows that are turned at a time
-    // an array a stage, so that waits are for the stage read, not for every fetch
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[SB], buf1[SB], buf2[D == 4 ? SB : 16],
         buf3[D == 4 ? SB : 16];
+    const Stages bufs = {{buf0, buf1, buf2, buf3}};
     __shared__ __attribute__((aligned(16))) unsigned char turn[W * 128 * TOK];
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
     __shared__ float sx_lds[2][Q ? BN : 64], rw_lds[BN];  // (x's scales of this tile and the next)
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN == 8 || RB == 64 ? 2 : 1
     Where cur = find(at);
     float *sx0 = sx_lds[0], *sx1 = sx_lds[1];
     TileRows op = operands(cur, sources(cur), sx0);
-    tile::begin(op, cb, wave, lane, buf0, buf1, buf2, buf3);
+    tile::begin(op, cb, wave, lane, bufs);
     for (;;) {
         // What the end needs comes into LDS under the products: no wave reads the tile
         // before any more.  (It is there when the first stages' barriers are passed.)
@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN == 8 || RB == 64 ? 2 : 1
         auto work = [&](auto blocks) {
             constexpr int NL = decltype(blocks)::value;
             typename tile::sum_t total[MB][NL];
-            tile::template sums<true, NL>(op, cb, wave, lane, buf0, buf1, buf2, buf3, total);
+            tile::template sums<true, NL>(op, cb, wave, lane, bufs, total);
             if (nxt.nrows) {
                 op = operands(nxt, far, sx1);
-                tile::begin(op, cb, wave, lane, buf0, buf1, buf2, buf3);
+                tile::begin(op, cb, wave, lane, bufs);
             }
 
             // as in k_linear_tile.hip: lane (hi, l32) holds channels 8j + 4hi + 0..3 of one row

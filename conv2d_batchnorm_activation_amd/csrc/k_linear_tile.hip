@@ -56,9 +56,9 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
     constexpr bool Q = X != kX16;  // 8-bit operands, tokens' scales
     constexpr unsigned XB = tile::XB;
     constexpr int NT = tile::NT, BM = tile::BM, BN = tile::BN, SB = tile::SB;
-    // an array a stage, so that waits are for the stage read, not for every fetch
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[SB], buf1[SB], buf2[D == 4 ? SB : 16],
         buf3[D == 4 ? SB : 16];
+    const Stages bufs = {{buf0, buf1, buf2, buf3}};
     __shared__ __attribute__((aligned(16))) float sc_lds[BM], bi_lds[BM];
     __shared__ float sx_lds[Q ? BN : 1];
     __shared__ int id_lds[LORA ? BN : 1];
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) k_linear_tile(Li
         if (LORA) id_lds[i] = adapter_of(a, token);
     }
     typename tile::sum_t total[MB][NB];
-    tile::template sums<false, NB>(op, cb, wave, lane, buf0, buf1, buf2, buf3, total);
+    tile::template sums<false, NB>(op, cb, wave, lane, bufs, total);
 
     // 32 tokens at a time; lane (hi, l32) holds channels 8j + 4hi + 0..3 of one
     // token.  A load waits for the stores before it, so finished values are kept,

@@ -30,6 +30,12 @@ struct TileRows {
     unsigned wo[8], xo[8];
 };
 
+// A tile's stage buffers, an array each, so that waits are for the stage read and not for
+// every fetch.
+struct Stages {
+    unsigned char* at[4];
+};
+
 // T: 16-bit type; X: what the operands are held in (kX16: T).  WM x WN waves, each
 // MB x NB blocks of 32 x 32; D stage buffers; a stage is RB bytes of every row.
 template <typename T, int X, int WM, int WN, int MB, int NB, int D, int RB = 128>
@@ -43,7 +49,7 @@ struct Tile {
     static constexpr int FM = BM / (RF * W), FN = BN / (RF * W);  // fetches a wave, per stage and operand
     static constexpr int STEPS = RB / (X8 ? 64 : 32);
     static constexpr int SB = (BM + BN) * RB;  // bytes of a stage
-    static_assert(D == 2 || D == 4, "stage buffers");
+    static_assert(W == 8 ? D == 2 && STEPS % 2 == 0 : W == 4 && D == 4, "stage buffers");
     static_assert(MB % 2 == 0, "values are stored 64 channels at a time");
     static_assert(W % 2 == 0, "a wave's fetches begin at rows 8 * wave + 16 * i");
     static_assert(FM <= 8 && FN <= 8, "fetches a wave");
@@ -87,15 +93,10 @@ struct Tile {
                                                      o.xo[i] | dead, 0, 0, 0);
     }
     // The first D stages.
-    static __device__ __forceinline__ void begin(const TileRows& o, unsigned cb, int wave, int lane, unsigned char* buf0,
-                                                 unsigned char* buf1, unsigned char* buf2, unsigned char* buf3)
+    static __device__ __forceinline__ void begin(const TileRows& o, unsigned cb, int wave, int lane, const Stages& bufs)
     {
-        issue(o, cb, 0, buf0, wave, lane);
-        issue(o, cb, 1, buf1, wave, lane);
-        if constexpr (D == 4) {
-            issue(o, cb, 2, buf2, wave, lane);
-            issue(o, cb, 3, buf3, wave, lane);
-        }
+#pragma unroll
+        for (int i = 0; i < D; ++i) issue(o, cb, i, bufs.at[i], wave, lane);
     }
 
     // The sums over all stages of rows of cb bytes, of the first 32*WN*NL rows of the
@@ -103,9 +104,8 @@ struct Tile {
     // BEGUN: the tile's first D stages are under way.  Else nothing is under way in LDS
     // before it, and after it nothing in either case.
     template <bool BEGUN, int NL>
-    static __device__ __forceinline__ void sums(const TileRows& o, unsigned cb, int wave, int lane,
-                                                unsigned char* buf0, unsigned char* buf1, unsigned char* buf2,
-                                                unsigned char* buf3, sum_t (&acc)[MB][NL])
+    static __device__ __forceinline__ void sums(const TileRows& o, unsigned cb, int wave, int lane, const Stages& bufs,
+                                                sum_t (&acc)[MB][NL])
     {
         const int wm = wave % WM, wn = wave / WM;
         const int hi = lane >> 5, l32 = lane & 31;
@@ -196,50 +196,33 @@ struct Tile {
             // those past the last are zeros, and so are the fetches past it.
             typedef std::integral_constant<int, 0> no_fetch;
             op_t A0[MB], B0[NL], A1[MB], B1[NL];
-            // A, B hold the first step's operands; where STEPS is odd, those of the next stage's
-            // first step are in An, Bn after it
-            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[MB], op_t(&B)[NL], op_t(&An)[MB],
-                             op_t(&Bn)[NL]) {
+            // A0, B0 hold the first step's operands, and those of the next stage's after it
+            auto stage = [&](int st, unsigned char* cur, unsigned char* nxt) {
 #pragma unroll
                 for (int s = 0; s + 1 < STEPS; ++s) {
                     if (s & 1) {
-                        read(cur, s + 1, A, B);
-                        mul(An, Bn);
+                        read(cur, s + 1, A0, B0);
+                        mul(A1, B1);
                     } else {
-                        read(cur, s + 1, An, Bn);
-                        mul(A, B);
+                        read(cur, s + 1, A1, B1);
+                        mul(A0, B0);
                     }
                     mix(no_fetch());
                 }
                 wait_arrived<(D - 2) * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
                 stage_barrier();
                 issue(st + D, cur);
-                if constexpr (STEPS & 1) {
-                    read(nxt, 0, An, Bn);
-                    mul(A, B);
-                } else {
-                    read(nxt, 0, A, B);
-                    mul(An, Bn);
-                }
+                read(nxt, 0, A0, B0);
+                mul(A1, B1);
                 mix(fetch());
             };
-            if constexpr (!BEGUN) begin(o, cb, wave, lane, buf0, buf1, buf2, buf3);
+            if constexpr (!BEGUN) begin(o, cb, wave, lane, bufs);
             wait_arrived<(D - 1) * (FM + FN)>();
             stage_barrier();
-            read(buf0, 0, A0, B0);
-            constexpr bool ODD = STEPS & 1;
-            op_t(&A2)[MB] = ODD ? A1 : A0, (&A3)[MB] = ODD ? A0 : A1;
-            op_t(&B2)[NL] = ODD ? B1 : B0, (&B3)[NL] = ODD ? B0 : B1;
-            for (int st = 0; st < nst; st += D) {
-                stage(st, buf0, buf1, A0, B0, A1, B1);
-                if constexpr (D == 2) {
-                    stage(st + 1, buf1, buf0, A2, B2, A3, B3);
-                } else {
-                    stage(st + 1, buf1, buf2, A2, B2, A3, B3);
-                    stage(st + 2, buf2, buf3, A0, B0, A1, B1);
-                    stage(st + 3, buf3, buf0, A2, B2, A3, B3);
-                }
-            }
+            read(bufs.at[0], 0, A0, B0);
+            for (int st = 0; st < nst; st += D)
+#pragma unroll
+                for (int i = 0; i < D; ++i) stage(st + i, bufs.at[i], bufs.at[(i + 1) % D]);
         } else {
             // One wave a SIMD: a stage's operands are all read under the stage before, as
             // a step's products (four instructions) are shorter than a read takes.
@@ -250,29 +233,24 @@ struct Tile {
             };
             auto stage = [&](int st, unsigned char* cur, unsigned char* nxt, op_t(&A)[STEPS][MB], op_t(&B)[STEPS][NL],
                              op_t(&An)[STEPS][MB], op_t(&Bn)[STEPS][NL]) {
-                wait_arrived<2 * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
+                wait_arrived<(D - 2) * (FM + FN)>();  // the next stage has arrived, this wave has read the current one
                 stage_barrier();
-                issue(st + 4, cur);
+                issue(st + D, cur);
                 read_all(nxt, An, Bn);
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) mul(A[s], B[s]);
                 mix_all();
             };
-            if constexpr (!BEGUN) {
-                issue(0, buf0);
-                issue(1, buf1);
-                issue(2, buf2);
-                issue(3, buf3);
-            }
-            wait_arrived<3 * (FM + FN)>();
+            if constexpr (!BEGUN) begin(o, cb, wave, lane, bufs);
+            wait_arrived<(D - 1) * (FM + FN)>();
             stage_barrier();
-            read_all(buf0, A0, B0);
-            for (int st = 0; st < nst; st += 4) {
-                stage(st, buf0, buf1, A0, B0, A1, B1);
-                stage(st + 1, buf1, buf2, A1, B1, A0, B0);
-                stage(st + 2, buf2, buf3, A0, B0, A1, B1);
-                stage(st + 3, buf3, buf0, A1, B1, A0, B0);
-            }
+            read_all(bufs.at[0], A0, B0);
+            for (int st = 0; st < nst; st += D)
+#pragma unroll
+                for (int i = 0; i < D; i += 2) {
+                    stage(st + i, bufs.at[i], bufs.at[i + 1], A0, B0, A1, B1);
+                    stage(st + i + 1, bufs.at[i + 1], bufs.at[(i + 2) % D], A1, B1, A0, B0);
+                }
         }
         wait_arrived<0>();  // no fetch is under way when LDS is used again
         stage_barrier();
