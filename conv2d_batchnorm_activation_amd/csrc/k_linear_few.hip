@@ -18,14 +18,15 @@
 // Measured, the rate that of the weights: one token, 4096 -> 4096 channels bf16 7.5
 // us (4.5 TB/s), with an adapter of rank 16 8.7; 16 tokens of e4m3, 8192 -> 8192
 // 15.0 (4.5), with 16 adapters of rank 16 21.3; 48 tokens bf16, 4096 -> 8192 16.6
-// (4.0), with 32 adapters of rank 32 34.  8-bit integers, summed as such: one token, 4096
-// -> 4096 4.4 to 5.8 (6.5 with the call), 48 tokens, 4096 -> 8192 with a residual 13.5
-// (2.6 TB/s: half the bytes between the same start and end).  A copy of such weights runs at 5.4 TB/s;
+// (4.0), with 32 adapters of rank 32 and a residual 32.7.  8-bit integers, summed as such: one token, 4096
+// -> 4096 4.4 to 5.8 (6.5 with the call), 48 tokens, 4096 -> 8192 with a residual 11.7
+// (2.9 TB/s: half the bytes between the same start and end, and x, which every
+// workgroup reads whole, is 196 KB to a compute unit beside 131 of weights).  A copy of such weights runs at 5.4 TB/s;
 // what is missing is a workgroup's first fetch and its end, as each compute unit
-// has one or two workgroups in all.  With a residual or adapters what the end needs
-// is loaded ahead of the first products (below), and only the stages fetched before
-// stand against that time: the 17 us between 34 and 16.6 are a launch for v, 5.4,
-// and 12 that the start and the end take longer.
+// has one or two workgroups in all.  With adapters what the end needs is loaded ahead
+// of the first products (below), and only the stages fetched before stand against that
+// time: the 16 us between 32.7 and 16.6 are a launch for v, 5.4, and 10.7 that the
+// start and the end take longer.
 #include "lin_common.h"
 
 #include "cvx_internal.h"
@@ -189,21 +190,24 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
     issue(2, st2);
     if constexpr (D == 4) issue(3, st3);
     // What the end needs is loaded here, behind the first stages' fetches and ahead of
-    // the first products.  Loads return in their order; each of the residual's, a 16-bit
-    // load behind a condition of its own, is waited for before the next, and v is joined
-    // from the newest.  So with these a workgroup's products begin once all of it is
-    // there.  A thread finishes one channel (c) of every TSTEP-th token.
+    // the first products.  The residual and x's scales have no branch, so nothing waits for
+    // them by itself (each 16-bit load behind a condition was waited for before the next:
+    // 48 tokens of integers, 4096 -> 8192, 13.5 us, 11.7 so); v is joined from the newest
+    // load, so with adapters a workgroup's products begin once all of it is there.  A thread
+    // finishes one channel (c) of every TSTEP-th token.
     constexpr int CH = 16 * RB, TSTEP = 64 * W / CH, ITEMS = (16 * NT + TSTEP - 1) / TSTEP;
     const int ch = tid % CH, tfirst = tid / CH, c = c0 + ch;
     const float sc = a.scale && c < a.cout ? a.scale[c] : 1.0f, bi = a.bias && c < a.cout ? a.bias[c] : 0.0f;
+    const rsrc_t rres = make_rsrc(a.res, a.res ? (unsigned)((a.tokens - 1) * a.rs + a.cout) * 2u : 0u);
+    const rsrc_t rsx = make_rsrc(a.x_scale, 4u * (unsigned)a.tokens);
     float sx[ITEMS];
-    T res[ITEMS];
+    unsigned short res[ITEMS];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         const int t = tfirst + TSTEP * k;
-        const bool ok = t < a.tokens && c < a.cout;
-        sx[k] = Q && ok ? a.x_scale[t] : 1.0f;
-        res[k] = a.res && ok ? static_cast<const T*>(a.res)[(long)t * a.rs + c] : (T)0.0f;
+        const unsigned off = c < a.cout ? ((unsigned)t * (unsigned)a.rs + (unsigned)c) * 2u : kOOB;
+        res[k] = __builtin_amdgcn_raw_buffer_load_b16(rres, (int)off, 0, 0);
+        sx[k] = Q ? bload(rsx, 4u * (unsigned)t) : 1.0f;
     }
     if (a.rank) {
         if (tid < 16 * NT) id_lds[tid] = id;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(64 * W) k_linear_few(LinArgs a)
         float z = (float)sum;  // of integers: rounded once from 2^24 up
         z = fmaf(Q ? z * sx[k] : z, sc, bi);
         if (a.rank) z += us[t * CH + ch];
-        static_cast<T*>(a.y)[(long)t * a.ys + c] = (T)finish(z, (float)res[k], a.act, a.res_mode);
+        static_cast<T*>(a.y)[(long)t * a.ys + c] = (T)finish(z, (float)__builtin_bit_cast(T, res[k]), a.act, a.res_mode);
     }
 }
 
