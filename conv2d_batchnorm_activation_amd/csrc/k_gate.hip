@@ -12,7 +12,8 @@
 // for the last bit of either, and then only the same roundings give the same code.  Few
 // values need 64 bits: those that may be the largest, and those that fp32 leaves at a
 // border.  With 64 bits for all (some 35 instructions a value) 8192 rows of 14336 bf16
-// channels took 236 us; they take 110, 5.3 TB/s.  Output of the inputs' type is u in
+// channels took 236 us; they take 110, 5.3 TB/s.  Still the vector units are busy most of
+// that time (31 instructions a value).  Output of the inputs' type is u in
 // fp32, and there is no row: a thread takes a vector.
 #include <type_traits>
 
@@ -32,17 +33,18 @@ __device__ __forceinline__ double act64(double g, bool relu)
 }
 
 // In fp32.  FAST: by the hardware's exponential and reciprocal (an ulp each), with what
-// rounding the exponential's argument, -g*log2(e), left as a factor: off by less than
-// 2*2^-23 + 4*2^-24 of the value where g is at least kDeep (below, 1/exp leaves fp32).
+// rounding the exponential's argument, x = -g*log2(e), left as a factor: off by less than
+// 2*2^-23 + 7*2^-24 of the value where g is at least kDeep (below, 1/exp leaves fp32; ln 2
+// in fp32 is off by 2^-28.4 of itself, |x| times 1.9e-9 in `left`, up to 4*2^-24 there).
 constexpr float kDeep = -80.0f;
 template <bool SILU, bool FAST>
 __device__ __forceinline__ float act32(float g, bool relu)
 {
     if constexpr (SILU && FAST) {
         const float x = g * -1.442695041f;
-        const float left = fmaf(g, -1.9259629911e-8f, fmaf(g, -1.442695041f, -x));
+        const float left = fmaf(x, -0.6931471806f, -g);
         const float e = __builtin_amdgcn_exp2f(x);
-        return g * __builtin_amdgcn_rcpf(1.0f + fmaf(e, left * 0.6931471806f, e));
+        return g * __builtin_amdgcn_rcpf(1.0f + fmaf(e, left, e));
     }
     if constexpr (SILU) {  // by the exponential that does not overflow: the value down to where fp32 ends
         const float e = expf(-fabsf(g));
@@ -63,8 +65,8 @@ __device__ __forceinline__ typename Vec<T, VEC>::type load_vec(const T* p, int i
     return v;
 }
 
-// More than an fp32 u*f is off by, of itself: u 2*2^-23 + 5*2^-24 with its second factor,
-// f half an ulp, twice and a half of the sum.
+// More than an fp32 u*f is off by, of itself: u 2*2^-23 + 8*2^-24 with its second factor,
+// f half an ulp; 1.8 times the sum.
 constexpr float kOff = 1.5f * 0x1p-20f;
 
 // How far u*f is off the integer next to it.
@@ -285,21 +287,33 @@ hipError_t launch_t(const GateArgs& a, hipStream_t s)
             hipLaunchKernelGGL((k_gate_wide<T, silu.value, up.value>), grid, dim3(256), 0, s, a);
         });
     } else if (nvec <= 16) {
-        // Short rows are 16 threads' or a wave's, which needs no barrier: us as 256 threads'
-        // rows and as these, 32768 rows of 1408 bf16 channels 85 and 47, 65536 of 512 (a wave
-        // each) 66 and 37, 500000 of 64 447 and 84.  Long ones are held as long as there
-        // are registers: 4096 of 20480 146 read anew, 108 held.
+        // The fewest threads that hold a row in registers, of 16, whole waves or workgroups
+        // (16 threads or a wave need no barrier), with little of them idle: more rows are then
+        // under way beside one that waits.  us, bf16 to integers, of some 10^8 values a case
+        // (390000 rows of 32 vectors, 3662 of 4096): 32 vectors 16x2 103, 16x4 115, 64x1 186; 96
+        // 64x2 111, 64x4 126; 256 64x4 109, 256x2 114; 640 256x3 108, 512x2 116, 1024x1 172;
+        // 1024 256x5 108, 512x2 107, 1024x1 131; 1280 256x5 110, 512x3 119, 1024x2 122; 1792
+        // 512x4 114, 256x8 119, 1024x2 112; 2560 512x5 113, 1024x4 151.  fp32, 3000 vectors
+        // 1024x3 68, 512x6 72, 1024x4 85.
         launch_rows<T, 16, 1>(a, s);
+    } else if (nvec <= 32) {
+        launch_rows<T, 16, 2>(a, s);
     } else if (nvec <= 64) {
         launch_rows<T, 16, 4>(a, s);
+    } else if (nvec <= 128) {
+        launch_rows<T, 64, 2>(a, s);
     } else if (nvec <= 256) {
         launch_rows<T, 64, 4>(a, s);
     } else if (nvec <= 512) {
         launch_rows<T, 256, 2>(a, s);
-    } else if (nvec <= 1024) {
-        launch_rows<T, 1024, 1>(a, s);
+    } else if (nvec <= 768) {
+        launch_rows<T, 256, 3>(a, s);
+    } else if (nvec <= 1280) {
+        launch_rows<T, 256, 5>(a, s);
     } else if (nvec <= 2048) {
-        launch_rows<T, 1024, 2>(a, s);
+        launch_rows<T, 512, 4>(a, s);
+    } else if (nvec <= (VEC == 8 ? 2560 : 3000)) {
+        launch_rows<T, VEC == 8 ? 512 : 1024, VEC == 8 ? 5 : 3>(a, s);
     } else if (nvec <= 4096) {
         launch_rows<T, 1024, 4>(a, s);
     } else if (VEC == 4 && nvec <= 6144) {

@@ -103,6 +103,18 @@ def test_gate(rows, c, dt, out):
     check(g, p, dt, out, (SILU, RELU, NONE)[k % 3] if k % 2 else SILU, ((5, 3, 1), (0, 0, 0), (8, 8, 16))[k % 3])
 
 
+# a row's vectors to where its threads, or the vectors each holds, change: of 8 values, and of 4
+WIDTHS = [n * v for v in (8, 4) for n in (16, 32, 64, 128, 256, 512, 768, 1280, 2048, 2560 if v == 8 else 3000, 4096)] + [24576]
+
+
+@pytest.mark.parametrize("c", WIDTHS)
+def test_row_widths(c):
+    dt, out = (BF16, I8) if c in WIDTHS[:11] else (F32, E4M3)
+    for n in (c - 1, c, c + 1):
+        g, p = rows_of(n, 19, n, dt)
+        check(g, p, dt, out, SILU, (0, 0, 0) if n % 2 else (4, 8, 4))
+
+
 @pytest.mark.parametrize("act", [NONE, RELU, SILU])
 @pytest.mark.parametrize("up", [False, True])
 @pytest.mark.parametrize("dt,out", [(BF16, E4M3), (F16, I8), (F32, E4M3), (BF16, BF16), (F32, F32)])
