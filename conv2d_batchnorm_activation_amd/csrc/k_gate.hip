@@ -286,16 +286,19 @@ hipError_t launch_t(const GateArgs& a, hipStream_t s)
         by_act(a, [&](auto silu, auto up) {
             hipLaunchKernelGGL((k_gate_wide<T, silu.value, up.value>), grid, dim3(256), 0, s, a);
         });
-    } else if (nvec <= 16) {
-        // The fewest threads that hold a row in registers, of 16, whole waves or workgroups
-        // (16 threads or a wave need no barrier), with little of them idle: more rows are then
+    } else if (nvec <= 8) {
+        // The fewest threads that hold a row in registers, of 8, 16, whole waves or
+        // workgroups (up to a wave needs no barrier), with little of them idle: more rows are then
         // under way beside one that waits.  us, bf16 to integers, of some 10^8 values a case
-        // (390000 rows of 32 vectors, 3662 of 4096): 32 vectors 16x2 103, 16x4 115, 64x1 186; 96
+        // (390000 rows of 32 vectors, 3662 of 4096): 8 vectors 8x1 167, 16x1 256; 16 8x2 121, 16x1
+        // 130; 32 16x2 103, 16x4 115, 64x1 186; 96
         // 64x2 111, 64x4 126; 256 64x4 109, 256x2 114; 640 256x3 108, 512x2 116, 1024x1 172;
         // 1024 256x5 108, 512x2 107, 1024x1 131; 1280 256x5 110, 512x3 119, 1024x2 122; 1792
         // 512x4 114, 256x8 119, 1024x2 112; 2560 512x5 113, 1024x4 151.  fp32, 3000 vectors
         // 1024x3 68, 512x6 72, 1024x4 85.
-        launch_rows<T, 16, 1>(a, s);
+        launch_rows<T, 8, 1>(a, s);
+    } else if (nvec <= 16) {
+        launch_rows<T, 8, 2>(a, s);
     } else if (nvec <= 32) {
         launch_rows<T, 16, 2>(a, s);
     } else if (nvec <= 64) {

@@ -108,7 +108,7 @@ __device__ __forceinline__ double wave_all(double v, OP op)
     return op(op(lane_value<0>(v), lane_value<16>(v)), op(lane_value<32>(v), lane_value<48>(v)));
 }
 
-// The largest of the values of a row's TPR threads (16, or whole waves), none of them a
+// The largest of the values of a row's TPR threads (8, 16 or whole waves), none of them a
 // NaN.  S: which of a kernel's exchanges by way of LDS this is.
 template <int TPR, int S, typename V>
 __device__ __forceinline__ V row_top(V v)
@@ -129,7 +129,7 @@ __device__ __forceinline__ V row_top(V v)
     v = larger(v, move(v, std::integral_constant<int, 0xb1>()));
     v = larger(v, move(v, std::integral_constant<int, 0x4e>()));
     v = larger(v, move(v, std::integral_constant<int, 0x141>()));
-    v = larger(v, move(v, std::integral_constant<int, 0x140>()));
+    if constexpr (TPR > 8) v = larger(v, move(v, std::integral_constant<int, 0x140>()));
     if constexpr (TPR > 16) {
         auto of = [&](auto lane) {
             if constexpr (F)

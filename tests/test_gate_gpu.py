@@ -104,12 +104,12 @@ def test_gate(rows, c, dt, out):
 
 
 # a row's vectors to where its threads, or the vectors each holds, change: of 8 values, and of 4
-WIDTHS = [n * v for v in (8, 4) for n in (16, 32, 64, 128, 256, 512, 768, 1280, 2048, 2560 if v == 8 else 3000, 4096)] + [24576]
+WIDTHS = [n * v for v in (8, 4) for n in (8, 16, 32, 64, 128, 256, 512, 768, 1280, 2048, 2560 if v == 8 else 3000, 4096)] + [24576]
 
 
 @pytest.mark.parametrize("c", WIDTHS)
 def test_row_widths(c):
-    dt, out = (BF16, I8) if c in WIDTHS[:11] else (F32, E4M3)
+    dt, out = (BF16, I8) if c in WIDTHS[:12] else (F32, E4M3)
     for n in (c - 1, c, c + 1):
         g, p = rows_of(n, 19, n, dt)
         check(g, p, dt, out, SILU, (0, 0, 0) if n % 2 else (4, 8, 4))
