@@ -74,6 +74,13 @@ def test_norm(rows, c, dt, res, pad):
     assert torch.equal(s.cpu(), h.to(DT[dt]))
 
 
+@pytest.mark.parametrize("c,dt", [(8193, BF16), (10240, F16), (10241, BF16), (16384, BF16), (16391, F16), (20480, BF16),
+                                  (20481, BF16), (4097, F32), (5120, F32), (5123, F32), (8192, F32), (8193, F32)])
+def test_norm_many_long_rows(c, dt):
+    # widths to where a row's threads, or the vectors each holds, change
+    test_norm(517, c, dt, c % 2 == 0, 3 * (c % 4))
+
+
 def test_norm_ties_and_limits():
     # half of the largest is 63.5 exactly: the even one of its neighbours
     x = torch.tensor([[2.0, 1.0, -1.0, -2.0, 0.0, 3 * 2.0 / 127, 2.0 / 127, 2.5]])
