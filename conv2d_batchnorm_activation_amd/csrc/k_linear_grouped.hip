@@ -12,7 +12,7 @@
 // groups' order.
 //
 // Few rows a group are bound by the weights' stream: 512 rows in 64 groups, 2048 -> 2816
-// e4m3 74 us, 5.1 TB/s of weights, a copy's rate; eight rows in eight groups, of integers
+// e4m3 74 us, 5.0 TB/s of weights, a copy's rate; eight rows in eight groups, of integers
 // 11.4, 4.1 TB/s.  Many rows are bound by the first touch of every group's weights: 64
 // groups of 512 rows, 2048 -> 2816 bf16 387 us (980 TFLOP/s), 318 as one group of as many
 // rows (1190), whose weights stay in the caches; e4m3 242, integers 233; 64 ragged groups
@@ -92,11 +92,11 @@ __device__ __forceinline__ void fetch64(rsrc_t r, unsigned off, void* to)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, (int)off, 0, 0, 0);
 }
 
-// WM x WN waves, each MB x NB blocks of 32 x 32; D stage buffers.
-template <typename T, int X, int WM, int WN, int MB, int NB, int D, int RB>
+// WM x WN waves, each MB x NB blocks of 32 x 32; D stage buffers; WIDE: e4m3 in 16 bits (lin_tile.h).
+template <typename T, int X, int WM, int WN, int MB, int NB, int D, int RB, bool WIDE>
 __global__ void __launch_bounds__(64 * WM * WN, WM * WN == 8 || RB == 64 ? 2 : 1) k_linear_grouped(GroupArgs a)
 {
-    typedef Tile<T, X, WM, WN, MB, NB, D, RB> tile;
+    typedef Tile<T, X, WM, WN, MB, NB, D, RB, WIDE> tile;
     typedef typename tile::v4 v4;
     constexpr bool Q = X != kX16;  // 8-bit operands, tokens' scales
     constexpr unsigned XB = tile::XB;
@@ -281,14 +281,21 @@ hipError_t launch_grouped_t(GroupArgs a, const GroupPlan& p, hipStream_t s)
 {
     a.tiles_m = (a.cout + 64 * p.mb - 1) / (64 * p.mb);
     const dim3 grid((unsigned)p.grid);
+    auto small = [&](auto wide) {
+        constexpr bool WIDE = decltype(wide)::value;
+        if (p.rb == 128)
+            hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 1, 4, 128, WIDE>), grid, dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 1, 4, 64, WIDE>), grid, dim3(256), 0, s, a);
+    };
     if (p.mb == 4)
-        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 4, 4, 2, 2, 128>), grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 4, 4, 2, 2, 128, false>), grid, dim3(512), 0, s, a);
     else if (p.nb == 2)
-        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 2, 4, 128>), grid, dim3(256), 0, s, a);
-    else if (p.rb == 128)
-        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 1, 4, 128>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 2, 4, 128, false>), grid, dim3(256), 0, s, a);
+    else if (X == kXE4m3 && p.wide)
+        small(std::integral_constant<bool, X == kXE4m3>());
     else
-        hipLaunchKernelGGL((k_linear_grouped<T, X, 2, 2, 2, 1, 4, 64>), grid, dim3(256), 0, s, a);
+        small(std::false_type());
     return hipGetLastError();
 }
 
@@ -324,7 +331,18 @@ GroupPlan grouped_plan(const cvx_grouped_desc& d)
     // 16 of 1024 -> 512 11.0 (9.2), eight of 2048 -> 1408 14.8 (12.9).
     const long blocks = (d.rows + 15 * some) / 16;  // of up to 16 rows, at most
     const long few = (long)((d.c_out + 15) / 16) * blocks;
-    p.few = few <= 256 || (few <= 512 && stages >= 32);
+    // Up to 64 rows a group on average are bound by the weights' stream where tiles are many:
+    // there e4m3 values are widened to 16 bits, whose sums are fp32.  64 groups, 2048 -> 2816,
+    // 8 rows each 73.9 us (72.6 by the 8-bit instructions), 33 81.0 (80.1), 64 90 (93); 128
+    // groups, 512 -> 768, 8 each 14.6 (13.8).  Where tiles are few, a stage's conversions stand
+    // beside its products: five groups of 30 rows, 1008 -> 1284, 9.0 us (7.1), 16 of 4, 2048 ->
+    // 1024, 12.2 (10.2).  Of long rows three and a half workgroups a compute unit of the kernel
+    // for few rows are faster then: two groups of 32 rows, 8192 -> 2048, 14.4 us (29.9 by
+    // widened tiles, 18.5 by the 8-bit instructions), three of 64, 8192 -> 1024, 19.6 (29.6,
+    // 19.6), ten of 8, 4096 -> 1024, 15.9 (17.9, 12.3); four a unit: one of 64, 4096 -> 4096,
+    // 20.3 (17.6, 12.5).  Tiles of 128 rows never are: 64 groups of 64 rows 98 us, of 64 rows 90.
+    p.wide = d.x_dtype == CVX_DT_E4M3 && d.rows <= 64l * d.n_groups;
+    p.few = few <= 256 || (few <= (p.wide ? 896 : 512) && stages >= 32);
     if (p.few) {
         p.mb = p.nb = p.rb = 0;
         p.grid = (int)blocks;
@@ -332,6 +350,7 @@ GroupPlan grouped_plan(const cvx_grouped_desc& d)
     }
     long best = -1;
     for (const auto& t : tiles) {
+        if (p.wide && t.nb > 1) continue;
         const long m = (d.c_out + 64 * t.mb - 1) / (64 * t.mb);
         const long tall = (d.rows + 64 * t.nb - 1) / (64 * t.nb) + some / 2, n = m * (tall < some ? some : tall);
         const long time = (n + t.at_once - 1) / t.at_once * (stages * t.stage + t.rest);

@@ -74,26 +74,29 @@ __device__ __forceinline__ i32x16 mma32_i8(u32x4 a, u32x4 b, i32x16 c)
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// eight e4m3 values or 8-bit integers -> eight 16-bit values, exactly
+// eight e4m3 values or 8-bit integers -> eight 16-bit values, exactly (e4m3: two values an
+// instruction; by way of fp32, two instructions, 512 rows in 64 groups 2048 -> 2816 took 78.5 us
+// instead of 73.9)
 template <typename T, int X>
 __device__ __forceinline__ u32x4 widen8(u32x2 q)
 {
-    typename V16<T>::v8 o;
     if constexpr (X == kXI8) {
+        typename V16<T>::v8 o;
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = (T)(float)(signed char)(q[i / 4] >> (8 * (i % 4)));
         return __builtin_bit_cast(u32x4, o);
     }
+    u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], false);
-        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i], true);
-        o[4 * i] = (T)lo[0];
-        o[4 * i + 1] = (T)lo[1];
-        o[4 * i + 2] = (T)hi[0];
-        o[4 * i + 3] = (T)hi[1];
-    }
-    return __builtin_bit_cast(u32x4, o);
+    for (int i = 0; i < 2; ++i)
+        if constexpr (V16<T>::BF) {
+            w[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], 1.0f, false));
+            w[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], 1.0f, true));
+        } else {
+            w[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[i], 1.0f, false));
+            w[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[i], 1.0f, true));
+        }
+    return w;
 }
 
 // 16x16 block, 64 bytes of k a row.  e4m3 values are widened to 16 bits, exactly:

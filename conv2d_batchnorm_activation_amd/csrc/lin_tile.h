@@ -37,8 +37,9 @@ struct Stages {
 };
 
 // T: 16-bit type; X: what the operands are held in (kX16: T).  WM x WN waves, each
-// MB x NB blocks of 32 x 32; D stage buffers; a stage is RB bytes of every row.
-template <typename T, int X, int WM, int WN, int MB, int NB, int D, int RB = 128>
+// MB x NB blocks of 32 x 32; D stage buffers; a stage is RB bytes of every row.  WIDE:
+// e4m3 values are widened to 16 bits, exactly, and multiplied as such.
+template <typename T, int X, int WM, int WN, int MB, int NB, int D, int RB = 128, bool WIDE = false>
 struct Tile {
     static constexpr bool X8 = X == kXE4m3;
     static constexpr bool I8 = X == kXI8;
@@ -53,6 +54,7 @@ struct Tile {
     static_assert(MB % 2 == 0, "values are stored 64 channels at a time");
     static_assert(W % 2 == 0, "a wave's fetches begin at rows 8 * wave + 16 * i");
     static_assert(FM <= 8 && FN <= 8, "fetches a wave");
+    static_assert(!WIDE || (X8 && W == 4), "values to widen");
     typedef typename V16<T>::v4 v4;
     typedef typename std::conditional<X8, i32x8, u32x4>::type op_t;
     // sums: of 8-bit integers exact ones
@@ -146,6 +148,21 @@ struct Tile {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0;
         auto mul = [&](const op_t(&A)[MB], const op_t(&B)[NL]) {
+            if constexpr (WIDE) {  // eight values of k a lane at a time
+#pragma unroll
+                for (int q = 0; q < 8; q += 2) {
+                    u32x4 b[NL];
+#pragma unroll
+                    for (int n = 0; n < NL; ++n) b[n] = widen8<T, X>(u32x2{(unsigned)B[n][q], (unsigned)B[n][q + 1]});
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
+                        const u32x4 a = widen8<T, X>(u32x2{(unsigned)A[m][q], (unsigned)A[m][q + 1]});
+#pragma unroll
+                        for (int n = 0; n < NL; ++n) acc[m][n] = mma32<T>(a, b[n], acc[m][n]);
+                    }
+                }
+                return;
+            }
 #pragma unroll
             for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -177,7 +194,8 @@ struct Tile {
             }
         };
         auto mix_all = [&]() {  // the same for a whole stage
-            constexpr int READS = (X8 ? 2 : 1) * (MB + NL) * STEPS, MUL = MB * NL * STEPS, OTHER = READS + FM + FN;
+            constexpr int READS = (X8 ? 2 : 1) * (MB + NL) * STEPS, MUL = (WIDE ? 4 : 1) * MB * NL * STEPS;
+            constexpr int OTHER = READS + FM + FN;
 #pragma unroll
             for (int i = 0; i < MUL; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);

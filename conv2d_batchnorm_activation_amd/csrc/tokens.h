@@ -123,6 +123,7 @@ struct GroupPlan {
     int few;               // 1: the kernel for few rows of few groups; 0: the tile kernel
     int mb, nb;            // tile: 64*mb channels x 64*nb rows
     int rb;                // bytes of a row a stage
+    int wide;              // tile: e4m3 values are multiplied in 16 bits
     int grid;              // tile: workgroups, a multiple of eight; few: blocks of rows
 };
 

@@ -522,7 +522,8 @@ CVX_API cvx_status cvx_linear_grouped_plan(const cvx_grouped_desc *d, char *buf,
  * one below an end before it as the largest before it.  Rows before the first group or
  * behind the last are left as they are.  A row whose row_id is negative or not below
  * `tokens` is taken as zeros.  Sums are those of cvx_linear: exact for 8-bit integers,
- * else in fp32, of e4m3 operands as it says for more than 64 tokens.  y is rounded once.
+ * else in fp32, of e4m3 operands too where rows is at most 64 * n_groups; above, as it
+ * says for more than 64 tokens.  y is rounded once.
  * A group's weights, infinities and NaN included, reach its rows and no others, and so
  * does a row of x; a NaN stays one through every activation.  Results do not depend on
  * timing.
