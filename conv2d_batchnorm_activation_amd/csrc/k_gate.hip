@@ -3,6 +3,7 @@
 //
 //     u = act(g) * up   (act(g) alone without `up`),   y = u rounded
 //     8 bits: t = max|u|, code = nearest(u*(M*(1/t))), scale = t/M, M = 448 or 127
+//     (M*(1/t) infinite: zeros)
 //
 // Bound by memory: every value is read once and written once.  With 8-bit output a
 // row's largest magnitude is one reduction between the TPR threads that hold it, as NV
@@ -188,7 +189,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 4) k_gate
     if (bad != 0.0) t = __builtin_inf();
     t = row_top<TPR, 1>(t);
     const bool lost = t > 1.7e308;
-    const double f = t > 0.0 && !lost ? kTop<OUT> * (1.0 / t) : 0.0;
+    // t = 0, or so small that M*(1/t) is infinite, which times a zero would be a NaN: zeros, and so is the scale
+    const double m = kTop<OUT> * (1.0 / t), f = lost || m == __builtin_inf() ? 0.0 : m;
     if (lane == 0) a.y_scale[row] = lost ? __builtin_nanf("") : (float)(t * (1.0 / kTop<OUT>));
 
     // codes from fp32 where it tells them, else from 64 bits

@@ -409,7 +409,8 @@ typedef struct cvx_gate_desc {
  *     u = act(gate) * up          (u = act(gate) without `up`)
  * and y = u, taken in fp32 and rounded once; or, with 8-bit output, t = max_i |u_i| of
  * the row and M = 448 (e4m3) or 127 (integers),
- *     y_i = code(u_i * (M * (1/t))),  y_scale = t/M     (t = 0: zeros)
+ *     y_i = code(u_i * (M * (1/t))),  y_scale = t/M
+ * (zeros where t is 0 or so small, below 2.5e-306, that M * (1/t) is infinite),
  * every step in 64 bits: the nearest e4m3 value or integer, ties to even, as cvx_rmsnorm
  * writes them and cvx_linear reads them.  With CVX_ACT_NONE and no `up`, rows are
  * brought to 8 bits as they are.  gate and up may be halves of one tensor, the output
