@@ -4,7 +4,7 @@
 // against it: an out-of-range load returns 0 and an out-of-range store is
 // dropped.  Kernels use this for zero padding and edge masking without branches
 // or per-element selects: an invalid element gets an offset >= 2^31, past any
-// tensor this library accepts (the host limits every buffer to < 2^31 bytes).
+// descriptor (the host limits what one covers to 2^31 bytes).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -13,7 +13,7 @@ namespace cvx {
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
-// Offset that is out of range for every descriptor (sizes are < 2^31 bytes).
+// Offset that is out of range for every descriptor (sizes are at most 2^31 bytes).
 constexpr unsigned kOOB = 0x80000000u;
 
 // Word 3 of a raw (untyped, stride 0) buffer descriptor on gfx9-family GPUs:
