@@ -289,15 +289,19 @@ hipError_t launch_t(const GateArgs& a, hipStream_t s)
             hipLaunchKernelGGL((k_gate_wide<T, silu.value, up.value>), grid, dim3(256), 0, s, a);
         });
     } else if (nvec <= 8) {
-        // The fewest threads that hold a row in registers, of 8, 16, whole waves or
-        // workgroups (up to a wave needs no barrier), with little of them idle: more rows are then
-        // under way beside one that waits.  us, bf16 to integers, of some 10^8 values a case
-        // (390000 rows of 32 vectors, 3662 of 4096): 8 vectors 8x1 167, 16x1 256; 16 8x2 121, 16x1
-        // 130; 32 16x2 103, 16x4 115, 64x1 186; 96
-        // 64x2 111, 64x4 126; 256 64x4 109, 256x2 114; 640 256x3 108, 512x2 116, 1024x1 172;
-        // 1024 256x5 108, 512x2 107, 1024x1 131; 1280 256x5 110, 512x3 119, 1024x2 122; 1792
-        // 512x4 114, 256x8 119, 1024x2 112; 2560 512x5 113, 1024x4 151.  fp32, 3000 vectors
-        // 1024x3 68, 512x6 72, 1024x4 85.
+        // Up to 1280 vectors the fewest threads that hold a row in registers, of 8, 16, whole
+        // waves or workgroups (up to a wave needs no barrier), with little of them idle: more
+        // rows are then under way beside one that waits.  us, bf16 to integers, of some 10^8
+        // values a case (390000 rows of 32 vectors, 3662 of 4096): 8 vectors 8x1 167, 16x1 256;
+        // 16 8x2 121, 16x1 130; 32 16x2 103, 16x4 115, 64x1 186; 96 64x2 111, 64x4 126; 256 64x4
+        // 109, 256x2 114; 640 256x3 108, 512x2 116, 1024x1 172; 1024 256x5 108, 512x2 107, 1024x1
+        // 131; 1280 256x5 110, 512x3 119, 1024x2 122.
+        // Longer rows by what measured less, 1.17*10^8 values of bf16 a case, half of fp32, to
+        // integers (to e4m3 the same order): bf16 1281 vectors 1024x2 125, 512x4 129; 1792 106 and
+        // 111 (64 rows 6.0 and 6.6, 1024 16.7 and 18.3); 2048 105 and 110; 2304 512x5 108, 1024x3
+        // 146 (256 rows 10.1 and 9.2); 2600 1024x3 142, 1024x4 145.  fp32 1300 512x4 95, 1024x2
+        // 101; 1700 94.0 and 94.9; 1792 95.6 and 94.6; 2049 1024x3 99, 512x5 101; 3000 97, 1024x4
+        // 118.
         launch_rows<T, 8, 1>(a, s);
     } else if (nvec <= 16) {
         launch_rows<T, 8, 2>(a, s);
@@ -315,10 +319,14 @@ hipError_t launch_t(const GateArgs& a, hipStream_t s)
         launch_rows<T, 256, 3>(a, s);
     } else if (nvec <= 1280) {
         launch_rows<T, 256, 5>(a, s);
+    } else if (VEC == 4 && nvec < 1792) {
+        launch_rows<T, VEC == 4 ? 512 : 1024, VEC == 4 ? 4 : 2>(a, s);
     } else if (nvec <= 2048) {
-        launch_rows<T, 512, 4>(a, s);
-    } else if (nvec <= (VEC == 8 ? 2560 : 3000)) {
+        launch_rows<T, 1024, 2>(a, s);
+    } else if (VEC == 8 && nvec <= 2560) {
         launch_rows<T, VEC == 8 ? 512 : 1024, VEC == 8 ? 5 : 3>(a, s);
+    } else if (nvec <= 3 * 1024) {
+        launch_rows<T, 1024, 3>(a, s);
     } else if (nvec <= 4096) {
         launch_rows<T, 1024, 4>(a, s);
     } else if (VEC == 4 && nvec <= 6144) {
