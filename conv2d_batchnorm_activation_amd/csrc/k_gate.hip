@@ -5,17 +5,19 @@
 //     8 bits: t = max|u|, code = nearest(u*(M*(1/t))), scale = t/M, M = 448 or 127
 //     (M*(1/t) infinite: zeros)
 //
-// Bound by memory: every value is read once and written once.  With 8-bit output a
-// row's largest magnitude is one reduction between the TPR threads that hold it, as NV
-// 16-byte vectors an operand each; rows too long to be held (NV = 0) are read a second
-// time.  t and the codes are those of 64-bit values, by the formula's own steps: where
-// u/t is a ratio of small integers, u*(M*(1/t)) can be a border between two codes but
-// for the last bit of either, and then only the same roundings give the same code.  Few
-// values need 64 bits: those that may be the largest, and those that fp32 leaves at a
-// border.  With 64 bits for all (some 35 instructions a value) 8192 rows of 14336 bf16
-// channels took 236 us; they take 110, 5.3 TB/s.  Still the vector units are busy most of
-// that time (31 instructions a value).  Output of the inputs' type is u in
-// fp32, and there is no row: a thread takes a vector.
+// Bound by memory: every value is read once and written once.  With 8-bit output a row's
+// largest magnitude is one reduction between the TPR threads that hold it, as NV 16-byte
+// vectors an operand each; rows too long to be held (NV = 0) are read three times, for the
+// largest fp32 value, for t and for the codes (3000 rows of 40000 bf16 channels 310 us,
+// 4.3 TB/s of what is loaded; 32768 channels, held, 114).  t and the codes are those of
+// 64-bit values, by the formula's own steps: where u/t is a ratio of small integers,
+// u*(M*(1/t)) can be a border between two codes but for the last bit of either, and then
+// only the same roundings give the same code.  Few values need 64 bits: those that may be
+// the largest, and those that fp32 leaves at a border.  With 64 bits for all (some 35
+// instructions a value) 8192 rows of 14336 bf16 channels took 236 us; they take 106 to
+// 110, 5.3 to 5.5 TB/s.  Still the vector units are busy most of that time (31
+// instructions a value).  Output of the inputs' type is u in fp32, and there is no row: a
+// thread takes a vector.
 #include <type_traits>
 
 #include "cvx_internal.h"
