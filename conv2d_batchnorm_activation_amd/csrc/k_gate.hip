@@ -8,8 +8,8 @@
 // Bound by memory: every value is read once and written once.  With 8-bit output a row's
 // largest magnitude is one reduction between the TPR threads that hold it, as NV 16-byte
 // vectors an operand each; rows too long to be held (NV = 0) are read three times, for the
-// largest fp32 value, for t and for the codes (3000 rows of 40000 bf16 channels 310 us,
-// 4.3 TB/s of what is loaded; 32768 channels, held, 114).  t and the codes are those of
+// largest fp32 value, for t and for the codes (3000 rows of 40000 bf16 channels 233 us,
+// 6.7 TB/s of what is loaded and stored; 32768 channels, held, 114).  t and the codes are those of
 // 64-bit values, by the formula's own steps: where u/t is a ratio of small integers,
 // u*(M*(1/t)) can be a border between two codes but for the last bit of either, and then
 // only the same roundings give the same code.  Few values need 64 bits: those that may be
@@ -109,9 +109,14 @@ __device__ __forceinline__ bool codes32(const float (&u)[VEC], float most, float
     return off > 0.5f - (most * f + 1.0f) * kOff;
 }
 
+// Waves a SIMD that the registers are to leave room for: eight of up to two vectors (64 registers),
+// but of rows read again, with all there is to do, which would keep 21 of its registers in
+// memory (3000 rows of 40000 bf16 channels to integers 313 us, 234 so; to e4m3 219 and 237).
+constexpr int waves_of(int nv, bool all) { return nv > 2 || (nv == 0 && all) ? 4 : 8; }
+
 // 8-bit output: TPR threads a row.
 template <typename T, int TPR, int NV, bool SILU, bool UP, int OUT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, NV <= 2 ? 8 : 4) k_gate(GateArgs a)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, waves_of(NV, SILU && UP && OUT == kXI8)) k_gate(GateArgs a)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
     constexpr int HOLD = NV > 0 ? NV : 1;
