@@ -2,23 +2,27 @@
 // group's weights, groups of any size.
 //
 // The products are those of k_linear_tile.hip (weights the A operand, rows the B
-// operand, lin_tile.h has the loop).  How many rows a group has stands in device
-// memory, so the tiles are counted there: a workgroup stays for several tiles, begins
-// with a scan of the groups' ends, and finds a tile's group by its number.  The first
-// stages of its next tile arrive while a tile finishes; a group's last tile, where it
-// has half of the rows or fewer, takes half of the products; tiles that share weights are
-// neighbours (the three together: 64 ragged groups, 32768 rows, 2048 -> 2816 bf16 434 ->
-// 412 us).  Rows are read where they lie (row_id), so that tokens need no copy in the
-// groups' order.
+// operand, lin_tile.h has the loop). How many rows a group has stands in device memory,
+// so the tiles are counted there: a workgroup stays for several tiles, begins with a
+// scan of the groups' ends, and finds a tile's group by its number. The first stages of
+// its next tile are fetched as a tile's products end; in tiles of 256x256 of 16-bit
+// operands they arrive under the arithmetic of its end, in the others the compiler waits
+// for them before the end's operands are read from LDS. A group's last tile, where it
+// has half of the rows or fewer, takes half of the products; tiles that share weights
+// are neighbours (the three together: 64 ragged groups, 32768 rows, 2048 -> 2816 bf16
+// 434 -> 412 us). Rows are read where they lie (row_id), so that tokens need no copy in
+// the groups' order.
 //
 // Few rows a group are bound by the weights' stream: 512 rows in 64 groups, 2048 -> 2816
-// e4m3 74 us, 5.0 TB/s of weights, a copy's rate; eight rows in eight groups, of integers
-// 11.4, 4.1 TB/s.  Many rows are bound by the first touch of every group's weights: 64
-// groups of 512 rows, 2048 -> 2816 bf16 387 us (980 TFLOP/s), 318 as one group of as many
-// rows (1190), whose weights stay in the caches; e4m3 242, integers 233; 64 ragged groups
-// of 510 on average 418, the tiles not filled being some 8%.  A fetch past the XCD's cache
-// takes 1095 cycles there (502 of one group), and the matrix pipes are busy 0.47 of their
-// cycles (0.59).  Eight groups of 1024 rows, 4096 -> 14336 e4m3 470 (2040).
+// e4m3 74 us, 5.0 TB/s of weights, a copy's rate; eight rows in eight groups, of
+// integers 11.4, 4.1 TB/s. Many rows are bound by the first touch of every group's
+// weights: 64 groups of 512 rows, 2048 -> 2816 bf16 387 to 389 us (980 TFLOP/s), 318 to
+// 340 as one group of as many rows (1110 to 1190), whose weights stay in the caches;
+// e4m3 242 to 255, integers 233 to 239; 64 ragged groups of 512 on average 416 to 431,
+// the tiles not filled being some 8%. Of these the profiler has 577 cycles a read past a
+// compute unit's cache and 1149 MB past the XCDs', 403 and 781 of the one group, the
+// matrix pipes busy 0.38 and 0.41 of 2.4 GHz's cycles. Eight groups of 1024 rows, 4096
+// -> 14336 e4m3 470 to 483 (1990 to 2040).
 #include <stdio.h>
 
 #include "cvx_internal.h"
