@@ -37,7 +37,8 @@ def rows_and_weights(seed, rows, n, ci, co):
 @pytest.mark.parametrize("sizes,ci,co,gather", [
     ([7, 9, 0, 64, 13] * 13, 2048, 644, False),  # the kind of tile that most shapes of few rows a group take
     ([8] * 128, 512, 768, True), ([1] * 80, 1040, 516, True), ([64, 1, 63] * 3, 272, 2052, False),
-    ([33, 30, 64, 60], 1008, 1284, True), ([40, 2], 144, 8196, False), ([60] * 40, 528, 2052, True), ([5, 3], 4096, 64, False)])
+    ([33, 30, 64, 60], 1008, 1284, True), ([40, 2], 144, 8196, False), ([60] * 40, 528, 2052, True), ([5, 3], 4096, 64, False),
+    ([64] * 3, 272, 1284, False), ([1, 127], 1040, 2052, True), ([32, 32], 8192, 2048, False), ([64, 0, 128], 8192, 1024, True)])
 def test_small_products_beside_large_ones(sizes, ci, co, gather, dt):
     rows, n = sum(sizes), len(sizes)
     assert rows <= 64 * n
@@ -58,5 +59,5 @@ def test_small_products_beside_large_ones(sizes, ci, co, gather, dt):
                            row_id=None if ids is None else ids.to(torch.int32).to(DEV))
     got = y.cpu().double()
     small = want.abs() <= 256
-    assert small.double().mean() > 0.5
+    assert small.double().mean() > 0.3
     assert torch.equal(got[small], want[small]), f"{int((got != want)[small].sum())} of {int(small.sum())} differ"

@@ -3,7 +3,8 @@
 Every row of x and of w is `half` channels of 64 to 127, the same values in another order (one order for all
 rows, and negated in w), and sixteen channels of -3 to 3.  A sum climbs to some 2^28 by odd values and comes
 back to one of at most 144, which bf16 holds: results are equal, while fp32 sums, which have even
-values only from 2^24 up, would be off by hundreds.  Where eight waves share a row each still passes 2^25.
+values only from 2^24 up, are off by some hundreds.  Where eight waves share a row each still passes
+2^25, and fp32 sums of theirs are off by some ten.
 
 The longest rows there are, of -128 throughout, sum to 131056 * 2^14 = 2^31 - 2^18, a multiple of 2^18 below
 2^31 that fp32 holds; times a power of two the output is its rounding to the output's type."""
